@@ -70,8 +70,16 @@ typedef enum {
 /* Storage of the routed and shared expert weights. */
 typedef enum {
     NH_WEIGHTS_NATIVE = 0,    /* in the activation dtype (bf16 or float32)          */
-    NH_WEIGHTS_NVFP4 = 1      /* NVFP4, see nh_nvfp4_weight (needs dtype NH_BF16)   */
+    NH_WEIGHTS_NVFP4 = 1,     /* NVFP4, see nh_nvfp4_weight (needs dtype NH_BF16)   */
+    NH_WEIGHTS_FP8 = 2        /* E4M3 with a scale per 128 x 128 block, see
+                                 nh_fp8_weight (needs dtype NH_BF16)                */
 } nh_weight_format;
+
+/* Score of an expert, from its router logit (nh_moe_gate, nh_moe_route_scored). */
+typedef enum {
+    NH_SCORE_SIGMOID = 0,
+    NH_SCORE_SOFTMAX = 1      /* over all experts of the token */
+} nh_score_func;
 
 /*
  * One stacked NVFP4 weight tensor [n_mat][rows][cols] (W4A16, group size 16:
@@ -90,6 +98,19 @@ typedef struct {
     const uint8_t *scales;
     const float *global_scale;
 } nh_nvfp4_weight;
+
+/*
+ * One stacked FP8 weight tensor [n_mat][rows][cols]: element (m, r, c) =
+ * e4m3(codes[m][r][c]) * scales[m][r / 128][c / 128].
+ *   codes  [n_mat][rows][cols]: E4M3 (no infinities, 0x7F and 0xFF are NaN);
+ *   scales [n_mat][ceil(rows / 128)][ceil(cols / 128)]: float32, any value.
+ * Both are device pointers, 16-byte aligned.  The struct itself is a host
+ * struct.
+ */
+typedef struct {
+    const uint8_t *codes;
+    const float *scales;
+} nh_fp8_weight;
 
 /*
  * Block configuration.  Field names are the model's config.json / MLX
@@ -148,6 +169,11 @@ typedef struct {
     int32_t n_chunks;     /* token chunks of the permute histogram              */
     int32_t swap_ab;      /* 1: weights on the MMA M side (small T, or NVFP4)   */
     int32_t x_direct;     /* 1: the up projection reads x itself (no x_perm)    */
+    /* With NH_WEIGHTS_FP8, written by the up projection's call: x_perm holds the
+     * E4M3 codes of x ([T, H] with x_direct, else [rows, H] in permuted order) and
+     * behind them, 256-byte aligned, their scales float [.., ceil(H / 128)]; h
+     * holds the codes of relu^2(up) [rows, I], their scales and, with x_direct,
+     * relu^2(up) itself in float32.  swap_ab and x_direct are 1 up to 32 tokens. */
 } nh_moe_ws_layout;
 
 /* Validate a configuration (no device work). */
@@ -193,6 +219,18 @@ nh_status nh_moe_route_permute(const nh_moe_config *cfg, int64_t T, const void *
                                const float *w_router, const float *e_score_correction_bias,
                                int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes,
                                void *stream);
+
+/*
+ * nh_moe_route with the scores of `score_func`: the logits of nh_moe_route, then
+ * nh_moe_gate on them.  Same arguments, results and workspace; with
+ * NH_SCORE_SIGMOID it differs from nh_moe_route only where a choice hangs on the
+ * last bits of a float32 score, and in what nh_moe_gate says of a row that has
+ * non-finite logits.
+ */
+nh_status nh_moe_route_scored(const nh_moe_config *cfg, int32_t score_func, int64_t T,
+                              const void *x, const float *w_router,
+                              const float *e_score_correction_bias, int32_t *topk_idx,
+                              float *topk_w, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * nh_moe_route_noalloc: the router of nh_moe_route for decode-sized batches,
@@ -378,6 +416,125 @@ nh_status nh_moe_latent_in(const nh_moe_config *cfg, int64_t T, const void *x,
 nh_status nh_moe_latent_out(const nh_moe_config *cfg, int64_t T, const void *y_lat,
                             const void *w_latent_fc2, float *y_acc, void *ws_latent,
                             size_t ws_latent_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The router's choice from logits, and its gradient
+ * ------------------------------------------------------------------------ */
+
+/* Fields as in nh_moe_config; dtype is that of logits and d_logits. */
+typedef struct {
+    int32_t n_routed_experts;      /* E, at most 512                 */
+    int32_t n_group;               /* G, E % G == 0, at most 64      */
+    int32_t topk_group;            /* 1 <= topk_group <= G           */
+    int32_t num_experts_per_tok;   /* k, at most 32                  */
+    int32_t norm_topk_prob;        /* bool                           */
+    float routed_scaling_factor;   /* alpha, finite                  */
+    int32_t score_func;            /* nh_score_func                  */
+    int32_t group_score;           /* nh_group_score                 */
+    int32_t dtype;                 /* nh_dtype                       */
+} nh_moe_gate_config;
+
+/*
+ * Choice and weights of every token from its router logits.  With l the logits,
+ * NaN taken as -inf and +inf as the largest float32:
+ *   s = sigmoid(l), or softmax(l) over the token's E experts;
+ *   c = s + bias (bias [E] finite, or NULL = 0), -inf where l = -inf;
+ *   groups of E / n_group neighbouring experts by their largest c, or by the sum
+ *   of their two largest (one that has a single expert above -inf by that one);
+ *   the topk_group best groups, of them the k best experts, in (c desc, id asc)
+ *   order, groups with equal values by the lower group;
+ *   weights alpha s_j / sum of the chosen s (norm_topk_prob) or alpha s_j.
+ * Without a bias and a sum of two the choice goes by the logits, which order the
+ * experts as their scores do.  Otherwise it is the choice of scores computed in
+ * 64 bits.  The weights are float32, and do not lose experts whose scores all
+ * underflow: with norm_topk_prob they are the softmax of the chosen logits (or
+ * the sigmoids' ratio).  An expert with l = -inf is taken only where fewer than
+ * k others are left in the kept groups, and has weight 0; so has every expert of
+ * a token without one above -inf.
+ *   logits [T, E] dtype; topk_idx [T, k] int32 (out); topk_w [T, k] float32 (out).
+ * Results do not depend on scheduling; no workspace.
+ */
+nh_status nh_moe_gate(const nh_moe_gate_config *cfg, int64_t T, const void *logits,
+                      const float *e_score_correction_bias, int32_t *topk_idx, float *topk_w,
+                      void *stream);
+
+/*
+ * d_logits of a loss from d_topk_w, the choice topk_idx held fixed (the bias takes
+ * no part in the weights, so it has no gradient).  d_logits [T, E] is written
+ * whole: zeros for experts that are not chosen, except with softmax and without
+ * norm_topk_prob, where every score depends on every logit.  An expert that
+ * topk_idx names twice gets both parts; an id outside [0, E) takes no part.
+ *   logits [T, E] dtype, as given to nh_moe_gate; topk_idx [T, k] int32;
+ *   d_topk_w [T, k] float32; d_logits [T, E] dtype (out; rounded once).
+ * n_group, topk_group and group_score are checked but not used.
+ */
+nh_status nh_moe_gate_backward(const nh_moe_gate_config *cfg, int64_t T, const void *logits,
+                               const int32_t *topk_idx, const float *d_topk_w, void *d_logits,
+                               void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point (E4M3) with a scale per block of 128
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Quantize rows: per row and block of 128 features the scale is the least power
+ * of two s >= 2^-126 with max|x| <= 448 s (1 for a block of zeros), and the
+ * code is x / s rounded to E4M3 (nearest even; the quotient is exact).  Inf and
+ * NaN become the NaN code and do not count in the maximum.
+ *   x [T, K] dtype (NH_F32 or NH_BF16), K a multiple of 16; codes [T, K] (out);
+ *   scales [T, ceil(K / 128)] float32 (out).
+ */
+nh_status nh_fp8_quantize(int64_t T, int64_t K, const void *x, int32_t dtype, uint8_t *codes,
+                          float *scales, void *stream);
+
+/* The same over 128 x 128 blocks of w [n_mat, rows, cols]: an nh_fp8_weight.
+ * cols a multiple of 16. */
+nh_status nh_fp8_quantize_weight(int64_t n_mat, int64_t rows, int64_t cols, const void *w,
+                                 int32_t dtype, uint8_t *codes, float *scales, void *stream);
+
+/*
+ * y = x W^T with E4M3 operands: x is quantized as by nh_fp8_quantize, and
+ *   y[t, n] = sum over blocks b of 128 features of
+ *             s_x[t, b] s_w[n / 128, b] (codes of x[t] . codes of W[n] in block b)
+ * with float32 products and sums, rounded once to y's dtype.
+ *   x [T, K] x_dtype; w: nh_fp8_weight [1][N][K]; y [T, N] y_dtype (out);
+ *   N and K multiples of 16; ws: nh_fp8_linear_workspace_size bytes, 256-byte
+ *   aligned, holding a status word (cleared by the caller, once:
+ *   nh_moe_reset_status; this call records device faults in it) and the
+ *   quantized x.  Calls that may overlap need their own ws.
+ * Up to 32 tokens run as a GEMV over the weights, more on tensor-core tiles; for
+ * given inputs a result does not depend on scheduling.
+ */
+nh_status nh_fp8_linear_workspace_size(int64_t T, int64_t N, int64_t K, size_t *bytes);
+nh_status nh_fp8_linear(int64_t T, int64_t N, int64_t K, const void *x, int32_t x_dtype,
+                        const nh_fp8_weight *w, void *y, int32_t y_dtype, void *ws,
+                        size_t ws_bytes, void *stream);
+
+/*
+ * nh_moe_forward / nh_moe_experts_* / nh_moe_shared / nh_moe_shared_store with FP8
+ * weights (cfg->weight_format == NH_WEIGHTS_FP8): w_up [E][I][H], w_down [E][H][I],
+ * w_shared_up [1][S][H], w_shared_down [1][H][S].  x is quantized per (token, 128
+ * features); relu^2 of the up projection is quantized the same way from its
+ * float32 value (it is never rounded to bf16).  NaN passes through relu^2.
+ * Everything else as there: the permute before, float32 adds into y_acc, the
+ * routed workspace (nh_moe_ws_layout) and ws_shared (256-byte aligned).
+ */
+nh_status nh_moe_forward_fp8(const nh_moe_config *cfg, int64_t T, const void *x,
+                             const nh_fp8_weight *w_up, const nh_fp8_weight *w_down, void *ws,
+                             size_t ws_bytes, float *y_acc, void *stream);
+nh_status nh_moe_experts_up_fp8(const nh_moe_config *cfg, int64_t T, const void *x,
+                                const nh_fp8_weight *w_up, void *ws, size_t ws_bytes,
+                                void *stream);
+nh_status nh_moe_experts_down_fp8(const nh_moe_config *cfg, int64_t T,
+                                  const nh_fp8_weight *w_down, void *ws, size_t ws_bytes,
+                                  float *y_acc, void *stream);
+nh_status nh_moe_shared_fp8(const nh_moe_config *cfg, int64_t T, const void *x,
+                            const nh_fp8_weight *w_shared_up, const nh_fp8_weight *w_shared_down,
+                            float *y_acc, void *ws_shared, size_t ws_shared_bytes, void *stream);
+nh_status nh_moe_shared_store_fp8(const nh_moe_config *cfg, int64_t T, const void *x,
+                                  const nh_fp8_weight *w_shared_up,
+                                  const nh_fp8_weight *w_shared_down, float *y_acc,
+                                  void *ws_shared, size_t ws_shared_bytes, void *stream);
 
 /*
  * Clear the status word at the start of workspace `ws` (any of the

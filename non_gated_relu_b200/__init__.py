@@ -24,7 +24,10 @@ from . import build as _build
 __all__ = ["NHMoEError", "Config", "Layout", "config_from", "load", "validate", "workspace_size",
            "workspace_layout", "shared_workspace_size", "route", "route_noalloc", "route_permute", "permute", "forward", "experts_up", "experts_down", "shared", "forward_nvfp4", "shared_nvfp4", "nvfp4_weight",
            "zero_acc", "finalize", "latent_config", "latent_workspace_size",
-           "latent_in", "latent_out", "reset_status", "check_device", "selftest_timeout", "library_path", "NemotronHMoE"]
+           "latent_in", "latent_out", "GateConfig", "Fp8Weight", "gate_config", "gate",
+           "gate_backward", "route_scored", "fp8_weight", "fp8_quantize", "fp8_quantize_weight",
+           "fp8_linear", "fp8_linear_workspace_size", "forward_fp8", "experts_up_fp8",
+           "experts_down_fp8", "shared_fp8", "shared_store_fp8", "reset_status", "check_device", "selftest_timeout", "library_path", "NemotronHMoE"]
 
 NH_OK, NH_ERR_INVALID_ARG, NH_ERR_UNSUPPORTED, NH_ERR_CUDA, NH_ERR_TIMEOUT, NH_ERR_DEVICE_CHECK = range(6)
 STATUS_NAMES = {0: "NH_OK", 1: "NH_ERR_INVALID_ARG", 2: "NH_ERR_UNSUPPORTED", 3: "NH_ERR_CUDA",
@@ -56,7 +59,25 @@ class NvFp4Weight(ctypes.Structure):
                 ("global_scale", ctypes.c_void_p)]
 
 
-NH_WEIGHTS_NATIVE, NH_WEIGHTS_NVFP4 = 0, 1
+class Fp8Weight(ctypes.Structure):
+    """nh_fp8_weight: device pointers of one stacked FP8 tensor (and, on the Python
+    side, its shape and the tensors themselves)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class GateConfig(ctypes.Structure):
+    """nh_moe_gate_config."""
+    _fields_ = [("n_routed_experts", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("num_experts_per_tok", ctypes.c_int32),
+                ("norm_topk_prob", ctypes.c_int32), ("routed_scaling_factor", ctypes.c_float),
+                ("score_func", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+NH_WEIGHTS_NATIVE, NH_WEIGHTS_NVFP4, NH_WEIGHTS_FP8 = 0, 1, 2
+NH_SCORE_SIGMOID, NH_SCORE_SOFTMAX = 0, 1
+_WEIGHT_FORMATS = {"native": 0, "nvfp4": 1, "fp8": 2, 0: 0, 1: 1, 2: 2}
+_SCORE_FUNCS = {"sigmoid": 0, "softmax": 1, 0: 0, 1: 1}
 
 
 class Layout(ctypes.Structure):
@@ -81,8 +102,8 @@ def config_from(c, group_score: int = 0) -> Config:
                   int(bool(c.norm_topk_prob)), float(c.routed_scaling_factor),
                   NH_BF16 if dt in ("bf16", NH_BF16) else NH_F32,
                   int(getattr(c, "group_score", group_score)),
-                  NH_WEIGHTS_NVFP4 if getattr(c, "weight_format", "native") in ("nvfp4", 1)
-                  else NH_WEIGHTS_NATIVE, int(getattr(c, "latent_size", 0) or 0))
+                  _WEIGHT_FORMATS.get(getattr(c, "weight_format", "native"), NH_WEIGHTS_NATIVE),
+                  int(getattr(c, "latent_size", 0) or 0))
 
 
 _lock = threading.Lock()
@@ -95,7 +116,11 @@ _EXPORTS = ["nh_moe_validate", "nh_moe_workspace_size", "nh_moe_workspace_layout
             "nh_moe_zero_acc",
             "nh_moe_finalize",
             "nh_moe_latent_config", "nh_moe_latent_workspace_size", "nh_moe_latent_in",
-            "nh_moe_latent_out", "nh_moe_reset_status", "nh_moe_check_device",
+            "nh_moe_latent_out", "nh_moe_route_scored", "nh_moe_gate", "nh_moe_gate_backward",
+            "nh_fp8_quantize", "nh_fp8_quantize_weight", "nh_fp8_linear_workspace_size",
+            "nh_fp8_linear", "nh_moe_forward_fp8", "nh_moe_experts_up_fp8",
+            "nh_moe_experts_down_fp8", "nh_moe_shared_fp8", "nh_moe_shared_store_fp8",
+            "nh_moe_reset_status", "nh_moe_check_device",
             "nh_moe_selftest_timeout",
             "nh_last_error", "nh_version"]
 
@@ -114,6 +139,7 @@ def load():
         lib = ctypes.CDLL(path)
         P, S, I64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
         C = ctypes.POINTER(Config)
+        G, W8, I32 = ctypes.POINTER(GateConfig), ctypes.POINTER(Fp8Weight), ctypes.c_int32
         sig = {
             "nh_moe_validate": [C],
             "nh_moe_workspace_size": [C, I64, ctypes.POINTER(S)],
@@ -137,6 +163,18 @@ def load():
             "nh_moe_latent_workspace_size": [C, I64, ctypes.POINTER(S)],
             "nh_moe_latent_in": [C, I64, P, P, P, P, S, P],
             "nh_moe_latent_out": [C, I64, P, P, P, P, S, P],
+            "nh_moe_route_scored": [C, I32, I64, P, P, P, P, P, P, S, P],
+            "nh_moe_gate": [G, I64, P, P, P, P, P],
+            "nh_moe_gate_backward": [G, I64, P, P, P, P, P],
+            "nh_fp8_quantize": [I64, I64, P, I32, P, P, P],
+            "nh_fp8_quantize_weight": [I64, I64, I64, P, I32, P, P, P],
+            "nh_fp8_linear_workspace_size": [I64, I64, I64, ctypes.POINTER(S)],
+            "nh_fp8_linear": [I64, I64, I64, P, I32, W8, P, I32, P, S, P],
+            "nh_moe_forward_fp8": [C, I64, P, W8, W8, P, S, P, P],
+            "nh_moe_experts_up_fp8": [C, I64, P, W8, P, S, P],
+            "nh_moe_experts_down_fp8": [C, I64, W8, P, S, P, P],
+            "nh_moe_shared_fp8": [C, I64, P, W8, W8, P, P, S, P],
+            "nh_moe_shared_store_fp8": [C, I64, P, W8, W8, P, P, S, P],
             "nh_moe_check_device": [P, P],
             "nh_moe_reset_status": [P, P],
             "nh_moe_selftest_timeout": [P, ctypes.c_uint64, P],
@@ -326,6 +364,235 @@ def latent_out(cfg, T: int, y_lat, w_latent_fc2, y_acc, ws_latent, stream=None):
     c = config_from(cfg)
     _check(load().nh_moe_latent_out(ctypes.byref(c), T, _p(y_lat), _p(w_latent_fc2), _p(y_acc),
                                     _p(ws_latent), _nbytes(ws_latent), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The router's choice from logits, and FP8 (E4M3, a scale per block of 128).
+# These calls check what they are given: types, shapes, contiguity and device.
+# ---------------------------------------------------------------------------
+def _dt(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return NH_BF16
+    if t.dtype == torch.float32:
+        return NH_F32
+    raise TypeError(f"expected bfloat16 or float32, got {t.dtype}")
+
+
+class _Types:
+    """torch types by what they hold (torch is imported with the first call)"""
+    act = f32 = bf16 = i32 = f8 = None
+
+
+def _types():
+    if _Types.act is None:
+        import torch
+        _Types.f32, _Types.bf16 = (torch.float32,), (torch.bfloat16,)
+        _Types.i32, _Types.f8 = (torch.int32,), (torch.float8_e4m3fn, torch.uint8)
+        _Types.act = _Types.bf16 + _Types.f32
+    return _Types
+
+
+def _args(*specs):
+    """Check device tensors, each (name, tensor, types, shape); returns their pointers.
+    Types, shapes and layout of all come before the device of any."""
+    import torch
+    for name, t, dtypes, shape in specs:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors passed to libnhmoe must be contiguous")
+    out = []
+    for name, t, _, _ in specs:
+        ptr = t.data_ptr()
+        if ptr and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+        out.append(ptr or None)
+    return out
+
+
+def gate_config(n_routed_experts, num_experts_per_tok, n_group=1, topk_group=1,
+                norm_topk_prob=True, routed_scaling_factor=1.0, scoring_func="sigmoid",
+                group_score="max", dtype="f32") -> GateConfig:
+    """Config of ``gate`` / ``gate_backward``: scoring_func "sigmoid" or "softmax",
+    group_score "max" or "top2", dtype ("f32" or "bf16") of the logits."""
+    try:
+        score, group = _SCORE_FUNCS[scoring_func], {"max": 0, "top2": 1, 0: 0, 1: 1}[group_score]
+        dt = {"f32": NH_F32, "bf16": NH_BF16, NH_F32: NH_F32, NH_BF16: NH_BF16}[dtype]
+    except KeyError as e:
+        raise ValueError(f"unknown scoring_func, group_score or dtype {e}") from None
+    return GateConfig(int(n_routed_experts), int(n_group), int(topk_group),
+                      int(num_experts_per_tok), int(bool(norm_topk_prob)),
+                      float(routed_scaling_factor), score, group, dt)
+
+
+def gate(cfg: GateConfig, logits, bias, topk_idx, topk_w, stream=None):
+    """Choice and weights of every token from its router logits [T, E] (nh_moe_gate):
+    writes topk_idx [T, k] int32 and topk_w [T, k] float32."""
+    ty = _types()
+    T, E, k = logits.shape[0], cfg.n_routed_experts, cfg.num_experts_per_tok
+    specs = [("logits", logits, ty.bf16 if cfg.dtype == NH_BF16 else ty.f32, (T, E)),
+             ("topk_idx", topk_idx, ty.i32, (T, k)), ("topk_w", topk_w, ty.f32, (T, k))]
+    if bias is not None:
+        specs.append(("bias", bias, ty.f32, (E,)))
+    ptrs = _args(*specs)
+    _check(load().nh_moe_gate(ctypes.byref(cfg), T, ptrs[0], ptrs[3] if bias is not None else None,
+                              ptrs[1], ptrs[2], _stream(stream)))
+
+
+def gate_backward(cfg: GateConfig, logits, topk_idx, d_topk_w, d_logits, stream=None):
+    """Gradient of the logits from that of topk_w (nh_moe_gate_backward): writes
+    d_logits [T, E], in the logits' type."""
+    ty = _types()
+    T, E, k = logits.shape[0], cfg.n_routed_experts, cfg.num_experts_per_tok
+    lt = ty.bf16 if cfg.dtype == NH_BF16 else ty.f32
+    ptrs = _args(("logits", logits, lt, (T, E)), ("topk_idx", topk_idx, ty.i32, (T, k)),
+                 ("d_topk_w", d_topk_w, ty.f32, (T, k)), ("d_logits", d_logits, lt, (T, E)))
+    _check(load().nh_moe_gate_backward(ctypes.byref(cfg), T, *ptrs, _stream(stream)))
+
+
+def route_scored(cfg, scoring_func, x, w_router, bias, topk_idx, topk_w, ws, stream=None):
+    """route with the scores of scoring_func ("sigmoid" or "softmax")."""
+    c = config_from(cfg)
+    if scoring_func not in _SCORE_FUNCS:
+        raise ValueError(f"unknown scoring_func {scoring_func!r}")
+    _check(load().nh_moe_route_scored(ctypes.byref(c), _SCORE_FUNCS[scoring_func], x.shape[0],
+                                      _p(x), _p(w_router), _p(bias), _p(topk_idx), _p(topk_w),
+                                      _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def fp8_weight(codes, scales) -> Fp8Weight:
+    """Struct of one FP8 tensor: codes [n, rows, cols] (float8_e4m3fn or uint8) and
+    scales [n, ceil(rows / 128), ceil(cols / 128)] float32.  It keeps the tensors alive."""
+    ty = _types()
+    if codes.dim() != 3:
+        raise ValueError(f"codes: expected [n, rows, cols], got {tuple(codes.shape)}")
+    n, rows, cols = codes.shape
+    w = Fp8Weight(*_args(("codes", codes, ty.f8, (n, rows, cols)),
+                         ("scales", scales, ty.f32, (n, -(-rows // 128), -(-cols // 128)))))
+    w.shape, w.tensors = (n, rows, cols), (codes, scales)
+    return w
+
+
+def _fp8(name, w, shape):
+    if not isinstance(w, Fp8Weight):
+        raise TypeError(f"{name}: expected fp8_weight(codes, scales), got {type(w).__name__}")
+    got = getattr(w, "shape", None)
+    if got is not None and got != tuple(shape):
+        raise ValueError(f"{name}: expected codes of shape {tuple(shape)}, got {got}")
+    return ctypes.byref(w)
+
+
+def fp8_quantize(x, codes, scales, stream=None):
+    """Rows x [T, K] (bfloat16 or float32) to E4M3 codes [T, K] and power-of-two scales
+    [T, ceil(K / 128)] (nh_fp8_quantize)."""
+    ty = _types()
+    T, K = x.shape
+    px, pc, ps = _args(("x", x, ty.act, (T, K)), ("codes", codes, ty.f8, (T, K)),
+                       ("scales", scales, ty.f32, (T, -(-K // 128))))
+    _check(load().nh_fp8_quantize(T, K, px, _dt(x), pc, ps, _stream(stream)))
+
+
+def fp8_quantize_weight(w, codes=None, scales=None, stream=None):
+    """w [n, rows, cols] (bfloat16 or float32) as FP8: returns (codes, scales), which
+    are allocated where they are not given."""
+    import torch
+    ty = _types()
+    if w.dim() != 3:
+        raise ValueError(f"w: expected [n, rows, cols], got {tuple(w.shape)}")
+    n, rows, cols = w.shape
+    blocks = (n, -(-rows // 128), -(-cols // 128))
+    if codes is None:
+        codes = torch.empty((n, rows, cols), dtype=torch.float8_e4m3fn, device=w.device)
+    if scales is None:
+        scales = torch.empty(blocks, dtype=torch.float32, device=w.device)
+    pw, pc, ps = _args(("w", w, ty.act, (n, rows, cols)), ("codes", codes, ty.f8, (n, rows, cols)),
+                       ("scales", scales, ty.f32, blocks))
+    _check(load().nh_fp8_quantize_weight(n, rows, cols, pw, _dt(w), pc, ps, _stream(stream)))
+    return codes, scales
+
+
+def fp8_linear_workspace_size(T: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().nh_fp8_linear_workspace_size(T, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def fp8_linear(x, w: Fp8Weight, y, ws, stream=None):
+    """y [T, N] = x [T, K] W^T with E4M3 operands (nh_fp8_linear); w holds one [N, K]
+    matrix, ws fp8_linear_workspace_size bytes (its status word cleared once by the
+    caller: torch.zeros or reset_status)."""
+    ty = _types()
+    T, K = x.shape
+    N = y.shape[1]
+    ref = _fp8("w", w, (1, N, K))
+    px, py = _args(("x", x, ty.act, (T, K)), ("y", y, ty.act, (T, N)))
+    _check(load().nh_fp8_linear(T, N, K, px, _dt(x), ref, py, _dt(y), _p(ws), _nbytes(ws),
+                                _stream(stream)))
+
+
+def _f8_args(c, x, y_acc):
+    """(T, pointer of x or None, pointer of y_acc or None)"""
+    ty = _types()
+    T = (x if x is not None else y_acc).shape[0]
+    specs = [] if x is None else [("x", x, ty.bf16, (T, c.hidden_size))]
+    if y_acc is not None:
+        specs.append(("y_acc", y_acc, ty.f32, (T, c.hidden_size)))
+    ptrs = _args(*specs)
+    return T, None if x is None else ptrs[0], None if y_acc is None else ptrs[-1]
+
+
+def forward_fp8(cfg, x, w_up: Fp8Weight, w_down: Fp8Weight, ws, y_acc, stream=None):
+    """forward with FP8 weights (fp8_weight structs): y_acc += routed experts of x."""
+    c = config_from(cfg)
+    T, px, py = _f8_args(c, x, y_acc)
+    E, H, I = c.n_routed_experts, c.hidden_size, c.moe_intermediate_size
+    _check(load().nh_moe_forward_fp8(ctypes.byref(c), T, px, _fp8("w_up", w_up, (E, I, H)),
+                                     _fp8("w_down", w_down, (E, H, I)), _p(ws), _nbytes(ws), py,
+                                     _stream(stream)))
+
+
+def experts_up_fp8(cfg, x, w_up: Fp8Weight, ws, stream=None):
+    c = config_from(cfg)
+    T, px, _ = _f8_args(c, x, None)
+    shape = (c.n_routed_experts, c.moe_intermediate_size, c.hidden_size)
+    _check(load().nh_moe_experts_up_fp8(ctypes.byref(c), T, px, _fp8("w_up", w_up, shape), _p(ws),
+                                        _nbytes(ws), _stream(stream)))
+
+
+def experts_down_fp8(cfg, T: int, w_down: Fp8Weight, ws, y_acc, stream=None):
+    c = config_from(cfg)
+    _, _, py = _f8_args(c, None, y_acc)
+    if y_acc.shape[0] != T:
+        raise ValueError(f"y_acc: expected {T} rows, got {y_acc.shape[0]}")
+    shape = (c.n_routed_experts, c.hidden_size, c.moe_intermediate_size)
+    _check(load().nh_moe_experts_down_fp8(ctypes.byref(c), T, _fp8("w_down", w_down, shape), _p(ws),
+                                          _nbytes(ws), py, _stream(stream)))
+
+
+def _shared_fp8(fn, cfg, x, w_su, w_sd, y_acc, ws_shared, stream):
+    c = config_from(cfg)
+    T, px, py = _f8_args(c, x, y_acc)
+    H, S = c.hidden_size, c.moe_shared_expert_intermediate_size
+    _check(fn(ctypes.byref(c), T, px, _fp8("w_shared_up", w_su, (1, S, H)),
+              _fp8("w_shared_down", w_sd, (1, H, S)), py, _p(ws_shared), _nbytes(ws_shared),
+              _stream(stream)))
+
+
+def shared_fp8(cfg, x, w_shared_up, w_shared_down, y_acc, ws_shared, stream=None):
+    """Shared expert with FP8 weights: y_acc += relu(x W_su^T)^2 W_sd^T."""
+    _shared_fp8(load().nh_moe_shared_fp8, cfg, x, w_shared_up, w_shared_down, y_acc, ws_shared,
+                stream)
+
+
+def shared_store_fp8(cfg, x, w_shared_up, w_shared_down, y_acc, ws_shared, stream=None):
+    """shared_fp8 as y_acc's starting value."""
+    _shared_fp8(load().nh_moe_shared_store_fp8, cfg, x, w_shared_up, w_shared_down, y_acc,
+                ws_shared, stream)
 
 
 def reset_status(ws, stream=None):

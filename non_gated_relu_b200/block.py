@@ -31,6 +31,11 @@ NemotronHMoELayerDescriptor) the routed experts run in width L:
     main: route(x) -> fc1: x_lat -> permute + forward into y_lat_acc      |
           -> y_lat = dtype(y_lat_acc) --+-> fc2: y_acc += y_lat W_fc2^T -> y = dtype(y_acc)
 
+The router's scores are the config's ``scoring_func``: "sigmoid" (also without the
+field) or "softmax", which routes with ``route_scored`` and then ``permute``.  FP8
+expert weights (``weight_format`` "fp8") follow the native order of calls, with the
+``_fp8`` entry points.
+
 All arithmetic happens in libnhmoe's kernels; this class only owns buffers,
 streams, events and (optionally) a CUDA graph of the call sequence.
 """
@@ -42,12 +47,15 @@ from typing import Dict, Optional
 import numpy as np
 import torch
 
-from . import (check_device, config_from, experts_down, experts_up, finalize, forward,
-               forward_nvfp4, latent_config,
+from . import (check_device, config_from, experts_down, experts_down_fp8, experts_up,
+               experts_up_fp8, finalize, forward,
+               forward_fp8, forward_nvfp4, fp8_weight, latent_config,
                latent_in, latent_out, latent_workspace_size, nvfp4_weight, permute, reset_status,
-               route, route_permute, shared, shared_nvfp4, shared_store, shared_workspace_size,
+               route, route_permute, route_scored, shared, shared_fp8, shared_nvfp4, shared_store,
+               shared_store_fp8, shared_workspace_size,
                validate,
-               workspace_layout, workspace_size, zero_acc, NH_BF16, NH_WEIGHTS_NVFP4)
+               workspace_layout, workspace_size, zero_acc, NH_BF16, NH_WEIGHTS_FP8,
+               NH_WEIGHTS_NVFP4)
 
 
 def _to_device(a, dtype: torch.dtype, device) -> torch.Tensor:
@@ -89,7 +97,10 @@ class NemotronHMoE:
     ``w_up [E, I, H]``, ``w_down [E, H, I]``, ``w_shared_up [S, H]``,
     ``w_shared_down [H, S]`` in the block dtype (bf16 or float32), and an
     optional router correction bias ``[E]`` float32.  numpy uint16 arrays are
-    taken as bf16 bit patterns.
+    taken as bf16 bit patterns.  With ``weight_format`` "nvfp4" or "fp8" the
+    expert weights come as ``nvfp4`` / ``fp8`` = {"up", "down", "shared_up",
+    "shared_down"} -> (codes, scales, global) / (codes, scales) instead, FP8 codes
+    [n, rows, cols] as float8_e4m3fn or uint8 (``fp8_quantize_weight`` makes them).
 
     libnhmoe launches on the current CUDA device, so call the block with its
     own device current (``torch.cuda.set_device`` or a ``torch.cuda.device``
@@ -98,7 +109,7 @@ class NemotronHMoE:
 
     def __init__(self, cfg, w_router, w_up=None, w_down=None, w_shared_up=None,
                  w_shared_down=None, bias=None, device=None, nvfp4=None, w_latent_fc1=None,
-                 w_latent_fc2=None):
+                 w_latent_fc2=None, fp8=None):
         self.cfg = cfg
         self.c = config_from(cfg)
         validate(self.c)
@@ -111,7 +122,11 @@ class NemotronHMoE:
         self.has_shared = bool(self.c.n_shared_experts)
         self.w_router = _to_device(w_router, torch.float32, self.device)
         self.bias = _to_device(bias, torch.float32, self.device)
+        self.scoring_func = getattr(cfg, "scoring_func", "sigmoid") or "sigmoid"
+        if self.scoring_func not in ("sigmoid", "softmax"):
+            raise ValueError(f"unknown scoring_func {self.scoring_func!r}")
         self.nvfp4 = self.c.weight_format == NH_WEIGHTS_NVFP4
+        self.fp8 = self.c.weight_format == NH_WEIGHTS_FP8
         if self.nvfp4:
             # {"up", "down", "shared_up", "shared_down"} -> (codes, scales, global)
             if nvfp4 is None:
@@ -126,6 +141,15 @@ class NemotronHMoE:
             self.w_up = self.w_down = self.w_shared_up = self.w_shared_down = None
             if self.has_shared and ("shared_up" not in self.q4 or "shared_down" not in self.q4):
                 raise ValueError("config has a shared expert but no shared weights were given")
+        elif self.fp8:
+            if fp8 is None:
+                raise ValueError("config has FP8 weights: pass fp8={...}")
+            # fp8_weight keeps the device tensors
+            with torch.cuda.device(self.device):
+                self.f8 = {name: fp8_weight(*(torch.as_tensor(a).to(self.device).contiguous()
+                                              for a in pair)) for name, pair in fp8.items()}
+            self._check_fp8()
+            self.w_up = self.w_down = self.w_shared_up = self.w_shared_down = None
         else:
             self.w_up = _to_device(w_up, self.dtype, self.device)
             self.w_down = _to_device(w_down, self.dtype, self.device)
@@ -153,6 +177,20 @@ class NemotronHMoE:
         self._bufs: Dict[int, Buffers] = {}
         self._graphs: Dict[int, tuple] = {}
         self._host: Dict[int, tuple] = {}
+
+    def _check_fp8(self):
+        c = self.c
+        H, I, S = c.latent_size or c.hidden_size, c.moe_intermediate_size, \
+            c.moe_shared_expert_intermediate_size
+        want = {"up": (c.n_routed_experts, I, H), "down": (c.n_routed_experts, H, I)}
+        if self.has_shared:
+            want.update(shared_up=(1, S, c.hidden_size), shared_down=(1, c.hidden_size, S))
+        for name, shape in want.items():
+            if name not in self.f8:
+                raise ValueError(f"config needs FP8 weight {name!r}")
+            if self.f8[name].shape != shape:
+                raise ValueError(f"fp8[{name!r}]: expected codes of shape {shape}, got "
+                                 f"{self.f8[name].shape}")
 
     # ------------------------------------------------------------------ buffers
     def buffers(self, T: int, slot: int = 0) -> Buffers:
@@ -210,8 +248,7 @@ class NemotronHMoE:
         route_first = not self.latent and not self.nvfp4 and T <= 32
         if route_first:
             push("route_permute")
-            route_permute(self.c, x, self.w_router, self.bias, b.topk_idx, b.topk_w, b.ws,
-                          stream=main)
+            self._route_permute(x, b, main)
             pop()
         if not store:
             # the accumulators start at zero on the side stream (beside the router)
@@ -228,7 +265,11 @@ class NemotronHMoE:
         # GEMMs take the SMs the routing and permute kernels leave idle)
         if self.has_shared:
             push("shared")
-            if self.nvfp4:
+            if self.fp8:
+                (shared_store_fp8 if store else shared_fp8)(
+                    self.c, x, self.f8["shared_up"], self.f8["shared_down"], b.y_acc, b.ws_shared,
+                    stream=self.side)
+            elif self.nvfp4:
                 shared_nvfp4(self.c, x, self.q4["shared_up"], self.q4["shared_down"], b.y_acc,
                              b.ws_shared, stream=self.side)
             elif store:
@@ -250,18 +291,26 @@ class NemotronHMoE:
             return out
         if not route_first:
             push("route_permute")
-            route_permute(self.c, x, self.w_router, self.bias, b.topk_idx, b.topk_w, b.ws,
-                          stream=main)
+            self._route_permute(x, b, main)
             pop()
         push("forward")
         if store:
             # y_acc holds the shared expert before the routed adds begin
-            experts_up(self.c, x, self.w_up, b.ws, stream=main)
+            if self.fp8:
+                experts_up_fp8(self.c, x, self.f8["up"], b.ws, stream=main)
+            else:
+                experts_up(self.c, x, self.w_up, b.ws, stream=main)
             shared_done()
-            experts_down(self.c, T, self.w_down, b.ws, b.y_acc, stream=main)
+            if self.fp8:
+                experts_down_fp8(self.c, T, self.f8["down"], b.ws, b.y_acc, stream=main)
+            else:
+                experts_down(self.c, T, self.w_down, b.ws, b.y_acc, stream=main)
         elif self.nvfp4:
             main.wait_event(zero)
             forward_nvfp4(self.c, x, self.q4["up"], self.q4["down"], b.ws, b.y_acc, stream=main)
+        elif self.fp8:
+            main.wait_event(zero)
+            forward_fp8(self.c, x, self.f8["up"], self.f8["down"], b.ws, b.y_acc, stream=main)
         else:
             main.wait_event(zero)
             forward(self.c, x, self.w_up, self.w_down, b.ws, b.y_acc, stream=main)
@@ -274,6 +323,15 @@ class NemotronHMoE:
         self._join(caller, main)
         return b.y_acc if partial else b.y
 
+    def _route_permute(self, x, b, main):
+        if self.scoring_func == "softmax":
+            route_scored(self.c, "softmax", x, self.w_router, self.bias, b.topk_idx, b.topk_w,
+                         b.ws, stream=main)
+            permute(self.c, x, b.topk_idx, b.topk_w, b.ws, stream=main)
+        else:
+            route_permute(self.c, x, self.w_router, self.bias, b.topk_idx, b.topk_w, b.ws,
+                          stream=main)
+
     @staticmethod
     def _join(caller, main):
         done = torch.cuda.Event()
@@ -283,7 +341,12 @@ class NemotronHMoE:
     def _forward_latent(self, x, b, main, zero, shared_done, partial, push, pop):
         T = x.shape[0]
         push("route")
-        route(self.c, x, self.w_router, self.bias, b.topk_idx, b.topk_w, b.ws_route, stream=main)
+        if self.scoring_func == "softmax":
+            route_scored(self.c, "softmax", x, self.w_router, self.bias, b.topk_idx, b.topk_w,
+                         b.ws_route, stream=main)
+        else:
+            route(self.c, x, self.w_router, self.bias, b.topk_idx, b.topk_w, b.ws_route,
+                  stream=main)
         pop()
         push("latent_in")
         latent_in(self.c, x, self.w_latent_fc1, b.x_lat, b.ws_lat, stream=main)
@@ -296,6 +359,9 @@ class NemotronHMoE:
         if self.nvfp4:
             forward_nvfp4(ce, b.x_lat, self.q4["up"], self.q4["down"], b.ws, b.y_lat_acc,
                           stream=main)
+        elif self.fp8:
+            forward_fp8(ce, b.x_lat, self.f8["up"], self.f8["down"], b.ws, b.y_lat_acc,
+                        stream=main)
         else:
             forward(ce, b.x_lat, self.w_up, self.w_down, b.ws, b.y_lat_acc, stream=main)
         finalize(ce, T, b.y_lat_acc, b.y_lat, stream=main)

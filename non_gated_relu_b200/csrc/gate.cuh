@@ -1,0 +1,527 @@
+// gate.cuh -- the router's choice from its logits, and its gradient.
+//
+// Per token, with l the logits as the router reads them (NaN counts as -inf,
+// an expert that cannot be taken; +inf as the largest float32):
+//   s = sigmoid(l)  or  softmax(l) over the E experts
+//   c = s + bias (bias selects only, it never enters a weight); -inf where l = -inf
+//   group value = its largest c, or the sum of its two largest (a missing second
+//   counts 0); the topk_group best groups stay; the k best experts of those,
+//   (c desc, id asc); groups tie to the lower group
+//   w_j = alpha s_j / sum of the chosen s   (norm)   or   alpha s_j
+//
+// The choice is that of exact scores.  Without a bias and without a sum over
+// two experts the logits order the experts as their scores do, so the float32
+// logits are compared themselves.  Otherwise c is computed in float32 first;
+// a token in which two neighbours that the choice or its order depends on are
+// closer than the float32 error of c (and are not the same logit and bias) is
+// chosen again from scores in 64 bits, by the same warp.
+//
+// Weights are computed from the chosen logits alone where norm is set, scaled
+// by the largest of them (softmax) or by min(0, largest) (sigmoid), so that
+// experts whose scores all underflow still share the token as they should.
+//
+// One warp per token; lane i holds experts [i PER, (i + 1) PER) in registers,
+// so the lowest lane that holds a maximum holds the lowest id.  A pick is one
+// integer max over the warp (redux) on order-preserving keys.
+#pragma once
+
+#include "common.cuh"
+
+namespace nh {
+namespace gate {
+
+constexpr int WARPS = 8;
+constexpr unsigned FULL = 0xffffffffu;
+
+struct Args {
+  const void* logits;     // [T, E] (float or bf16)
+  const float* bias;      // [E] or null
+  int32_t* idx;           // [T, k] out (forward), in (backward)
+  float* w;               // [T, k] out (forward)
+  const float* dw;        // [T, k] in (backward)
+  void* dlogits;          // [T, E] out (backward), the logits' type
+  int64_t T;
+  int E, G, tg, k;
+  int softmax, norm, top2;
+  float alpha;
+};
+
+__device__ __forceinline__ float clean(float l) {
+  return l != l ? -INFINITY : fminf(l, 3.402823466e38f) + 0.0f;   // -0 becomes +0: they tie
+}
+
+// order-preserving key of a float that is not NaN; 0 is below every key
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  return of_key(__reduce_max_sync(FULL, key_of(v)));
+}
+
+// Row values [lane PER, lane PER + PER), cleaned; -inf past E.  16-byte loads
+// where rows and lanes start on them.
+template <int PER>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, float (&l)[PER]) {
+  const int e0 = lane * PER;
+  if (PER >= 4 && (E % 4) == 0) {
+#pragma unroll
+    for (int i = 0; i + 3 < PER; i += 4) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e0 + i < E) v = __ldg(reinterpret_cast<const float4*>(row + e0 + i));
+      l[i] = clean(v.x);
+      l[i + 1] = clean(v.y);
+      l[i + 2] = clean(v.z);
+      l[i + 3] = clean(v.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? clean(__ldg(row + e0 + i)) : -INFINITY;
+  }
+}
+
+template <int PER>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* row, int E, int lane,
+                                         float (&l)[PER]) {
+  const int e0 = lane * PER;
+  if (PER >= 4 && (E % 4) == 0) {
+#pragma unroll
+    for (int i = 0; i + 3 < PER; i += 4) {
+      uint2 u = make_uint2(0xff80ff80u, 0xff80ff80u);   // -inf
+      if (e0 + i < E) u = __ldg(reinterpret_cast<const uint2*>(row + e0 + i));
+      l[i] = clean(__uint_as_float(u.x << 16));
+      l[i + 1] = clean(__uint_as_float(u.x & 0xffff0000u));
+      l[i + 2] = clean(__uint_as_float(u.y << 16));
+      l[i + 3] = clean(__uint_as_float(u.y & 0xffff0000u));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      l[i] = e0 + i < E ? clean(__bfloat162float(row[e0 + i])) : -INFINITY;
+  }
+}
+
+template <int PER>
+__device__ __forceinline__ void store_row(float* row, int E, int lane, const float (&v)[PER]) {
+  const int e0 = lane * PER;
+  if (PER >= 4 && (E % 4) == 0) {
+#pragma unroll
+    for (int i = 0; i + 3 < PER; i += 4)
+      if (e0 + i < E)
+        *reinterpret_cast<float4*>(row + e0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i < E) row[e0 + i] = v[i];
+  }
+}
+
+template <int PER>
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int E, int lane,
+                                          const float (&v)[PER]) {
+  const int e0 = lane * PER;
+  if (PER >= 4 && (E % 4) == 0) {
+#pragma unroll
+    for (int i = 0; i + 3 < PER; i += 4)
+      if (e0 + i < E)
+        *reinterpret_cast<uint2*>(row + e0 + i) =
+            make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i < E) row[e0 + i] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+// sigmoid without overflow or cancellation at either end
+__device__ __forceinline__ float sigmoid(float l) {
+  const float e = expf(-fabsf(l));
+  return l < 0.f ? e / (1.f + e) : 1.f / (1.f + e);
+}
+
+// This lane's part of the chosen experts' summed score: lanes j < k hold their
+// chosen logit l (-inf: cannot be taken, part 0), the others -inf.
+__device__ __forceinline__ float share(float l, bool softmax) {
+  float top = warp_max(l);
+  if (top == -INFINITY) top = 0.f;
+  float u;
+  if (softmax) {
+    u = expf(l - top);
+  } else {
+    // e^-m sigmoid(l), m = min(0, top): l >= 0 only where m = 0
+    const float m = fminf(top, 0.f);
+    u = l < 0.f ? expf(l - m) / (1.f + expf(l)) : sigmoid(l);
+  }
+  const float z = warp_sum(u);
+  return z > 0.f ? u / z : 0.f;
+}
+
+// value of a pair (largest, second largest) as a group value
+template <typename V>
+__device__ __forceinline__ V group_value(V v1, V v2, bool top2) {
+  return top2 && v2 != -INFINITY ? v1 + v2 : v1;
+}
+
+template <typename V>
+__device__ __forceinline__ void top2_add(V v, V& v1, V& v2) {
+  if (v > v1) {
+    v2 = v1;
+    v1 = v;
+  } else if (v > v2) {
+    v2 = v;
+  }
+}
+
+// Groups by value from shared memory, any group size: lane q reduces groups q
+// and q + 32, starting at its own place in the group so that the lanes' reads
+// spread over the banks.  Returns the kept groups as a mask; `close` (float)
+// is set where the last group kept and the first one dropped are within tol.
+template <typename V>
+__device__ __forceinline__ uint64_t keep_groups(const V* c, int G, int g, int tg, bool top2,
+                                                int lane, float tol_s, bool* close) {
+  V gs[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int q = lane + 32 * r;
+    V v1 = -INFINITY, v2 = -INFINITY;
+    if (q < G)
+      for (int i = 0, p = q % g; i < g; ++i) {
+        top2_add(c[q * g + p], v1, v2);
+        if (++p == g) p = 0;
+      }
+    gs[r] = group_value(v1, v2, top2);
+  }
+  int rank[2] = {0, 0};
+  for (int q = 0; q < G; ++q) {
+    const V o = __shfl_sync(FULL, q < 32 ? gs[0] : gs[1], q & 31);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int me = lane + 32 * r;
+      rank[r] += (o > gs[r] || (o == gs[r] && q < me)) ? 1 : 0;
+    }
+  }
+  uint64_t keep = 0;
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    keep |= (uint64_t)__ballot_sync(FULL, lane + 32 * r < G && rank[r] < tg) << (32 * r);
+  if (close && tg < G) {
+    // values of ranks tg - 1 and tg
+    V last = 0, next = 0;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool in = lane + 32 * r < G;
+      const unsigned a = __ballot_sync(FULL, in && rank[r] == tg - 1);
+      const unsigned b = __ballot_sync(FULL, in && rank[r] == tg);
+      const V va = __shfl_sync(FULL, gs[r], a ? __ffs(a) - 1 : 0);
+      const V vb = __shfl_sync(FULL, gs[r], b ? __ffs(b) - 1 : 0);
+      if (a) last = va;
+      if (b) next = vb;
+    }
+    // two group values that are both -inf tie exactly
+    *close = (float)(last - next) <= tol_s + 0x1p-22f * fabsf((float)last);
+  }
+  return keep;
+}
+
+// The choice from 64-bit scores (rare): writes pick j to lane j's `e`.
+template <int PER, typename Tin>
+__device__ __noinline__ int choose_f64(const Tin* row, const Args& a, double* c, int lane) {
+  const int E = a.E, g = E / a.G, e0 = lane * PER;
+  float l[PER];
+  load_row<PER>(row, E, lane, l);
+  double s[PER];
+  if (a.softmax) {
+    float mine = l[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) mine = fmaxf(mine, l[i]);
+    float top = warp_max(mine);
+    if (top == -INFINITY) top = 0.f;
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      s[i] = exp((double)l[i] - (double)top);
+      z += s[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s[i] = z > 0.0 ? s[i] / z : 0.0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+  }
+  uint32_t live = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = e0 + i;
+    if (e < E) {
+      s[i] = l[i] == -INFINITY ? -INFINITY : s[i] + (a.bias ? (double)a.bias[e] : 0.0);
+      c[e] = s[i];
+      live |= 1u << i;
+    }
+  }
+  __syncwarp();
+  if (a.tg < a.G) {
+    const uint64_t keep = keep_groups<double>(c, a.G, g, a.tg, a.top2, lane, 0.f, nullptr);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i < E && !((keep >> ((e0 + i) / g)) & 1ull)) live &= ~(1u << i);
+  }
+  int mine = 0;
+  for (int j = 0; j < a.k; ++j) {
+    double bv = 0.0;
+    int be = -1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (((live >> i) & 1u) && (be < 0 || s[i] > bv)) {
+        bv = s[i];
+        be = e0 + i;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double ov = __shfl_xor_sync(FULL, bv, o);
+      const int oe = __shfl_xor_sync(FULL, be, o);
+      if (oe >= 0 && (be < 0 || ov > bv || (ov == bv && oe < be))) {
+        bv = ov;
+        be = oe;
+      }
+    }
+    const int i = be - e0;
+    if (i >= 0 && i < PER) live &= ~(1u << i);
+    if (lane == j) mine = be;
+  }
+  return mine;
+}
+
+template <int PER, typename Tin>
+__global__ void __launch_bounds__(WARPS * 32) gate_forward(const Args a) {
+  extern __shared__ double smem[];   // [WARPS][E]
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x * (int64_t)WARPS + warp;
+  if (t >= a.T) return;
+  const int E = a.E, g = E / a.G, k = a.k, e0 = lane * PER;
+  const Tin* row = static_cast<const Tin*>(a.logits) + t * E;
+  float l[PER];
+  load_row<PER>(row, E, lane, l);
+
+  const bool grouped = a.tg < a.G;
+  const bool by_score = a.bias != nullptr || (grouped && a.top2);
+  float top = 0.f, z = 1.f;      // of the softmax over all experts
+  if (a.softmax && (by_score || !a.norm)) {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
+    top = warp_max(m);
+    if (top == -INFINITY) top = 0.f;
+    float p = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) p += expf(l[i] - top);
+    z = warp_sum(p);
+    if (z == 0.f) z = 1.f;
+  }
+  float c[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = l[i];
+    if (by_score && l[i] != -INFINITY) {
+      const float s = a.softmax ? expf(l[i] - top) / z : sigmoid(l[i]);
+      c[i] = s + (a.bias ? __ldg(a.bias + e0 + i) : 0.f) + 0.0f;
+    }
+  }
+  // Twice the float32 error of a score.  sigmoid: expf and a divide, under 4
+  // roundings of a value <= 1.  softmax: those, and up to PER + 5 adds of z, of
+  // a value <= 1 / z.  The add of the bias is counted at the comparison.
+  const float tol_s = a.softmax ? (PER + 10) * 0x1p-22f / z : 0x1p-20f;
+  bool again = false;
+
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = e0 + i < E ? key_of(c[i]) : 0u;
+  if (grouped) {
+    const int width = g / PER;
+    bool close = false;
+    if (g % PER == 0 && (width & (width - 1)) == 0) {
+      // a group is `width` whole lanes: its two largest by a butterfly
+      float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) top2_add(c[i], v1, v2);
+      for (int o = 1; o < width; o <<= 1) {
+        const float o1 = __shfl_xor_sync(FULL, v1, o), o2 = __shfl_xor_sync(FULL, v2, o);
+        v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
+        v1 = fmaxf(v1, o1);
+      }
+      const float gs = group_value(v1, v2, a.top2);
+      const int me = lane / width;
+      int rank = 0;
+      for (int q = 0; q < a.G; ++q) {
+        const float o = __shfl_sync(FULL, gs, q * width);
+        rank += (o > gs || (o == gs && q < me)) ? 1 : 0;
+      }
+      const bool in = me < a.G;
+      const unsigned la = __ballot_sync(FULL, in && rank == a.tg - 1);
+      const unsigned lb = __ballot_sync(FULL, in && rank == a.tg);
+      const float last = __shfl_sync(FULL, gs, __ffs(la) - 1);
+      const float next = __shfl_sync(FULL, gs, __ffs(lb) - 1);
+      close = last - next <= 2.f * tol_s + 0x1p-22f * fabsf(last);
+      if (rank >= a.tg) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = 0u;
+      }
+    } else {
+      float* cs = reinterpret_cast<float*>(smem + (size_t)warp * E);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E) cs[e0 + i] = c[i];
+      __syncwarp();
+      const uint64_t keep =
+          keep_groups<float>(cs, a.G, g, a.tg, a.top2, lane, 2.f * tol_s, &close);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E && !((keep >> ((e0 + i) / g)) & 1ull)) key[i] = 0u;
+    }
+    again = by_score && close;
+  }
+
+  // the k best, lane j the j-th; with scores one more, whose distance counts
+  int my_e = 0;
+  uint32_t my_key = 0u, next_key = 0u;
+  const int rounds = by_score ? k + 1 : k;
+  for (int j = 0; j < rounds; ++j) {
+    uint32_t bk = key[0];
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < PER; ++i)
+      if (key[i] > bk) {
+        bk = key[i];
+        bi = i;
+      }
+    const uint32_t m = __reduce_max_sync(FULL, bk);
+    const int src = __ffs(__ballot_sync(FULL, bk == m)) - 1;
+    const int e = __shfl_sync(FULL, e0 + bi, src);
+    if (lane == src) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i == bi) key[i] = 0u;
+    }
+    if (lane == j) {
+      my_e = e;
+      my_key = m;
+    }
+    if (j == k) next_key = m;   // the runner-up: in lane k too, if there is one
+  }
+  const auto logit_of = [&](int e) { return clean(to_f32(row[e])); };
+  if (by_score) {
+    // neighbours closer than the error of their scores, and not equal inputs
+    const float mine = of_key(my_key);
+    const float l_me = lane <= k ? logit_of(my_e) : 0.f;
+    const float b_me = lane <= k && a.bias ? a.bias[my_e] : 0.f;
+    uint32_t after = __shfl_down_sync(FULL, my_key, 1);
+    const float l_after = __shfl_down_sync(FULL, l_me, 1);
+    const float b_after = __shfl_down_sync(FULL, b_me, 1);
+    // equal inputs tie exactly and stay in id order; at the end of the k best
+    // they do not count as such, since what comes after the runner-up is not seen
+    const bool same = lane < k - 1 && l_me == l_after && b_me == b_after;
+    if (lane == 31) after = next_key;
+    const bool near = lane < k && after != 0u && !same && mine != -INFINITY &&
+                      mine - of_key(after) <= tol_s + 0x1p-22f * fabsf(mine);
+    again = again || __any_sync(FULL, near);
+    if (again) my_e = choose_f64<PER>(row, a, smem + (size_t)warp * E, lane);
+  }
+  const float lj = lane < k ? logit_of(my_e) : -INFINITY;
+  float wj;
+  if (a.norm)
+    wj = share(lj, a.softmax != 0);
+  else
+    wj = a.softmax ? expf(lj - top) / z : sigmoid(lj);
+  if (lane < k) {
+    a.idx[t * k + lane] = my_e;
+    a.w[t * k + lane] = a.alpha * wj;
+  }
+}
+
+// d logits from d weights.  With p_j the shares of the chosen experts and D =
+// sum p_j dw_j:
+//   norm, softmax   dl_j = alpha p_j (dw_j - D)
+//   norm, sigmoid   dl_j = alpha p_j (dw_j - D) (1 - s_j)
+//   raw,  sigmoid   dl_j = alpha dw_j s_j (1 - s_j)
+//   raw,  softmax   dl_i = alpha s_i ([i chosen] dw_i - sum_j s_j dw_j), every i
+// (from dw = alpha d(s_j / sum s): d log p_j = d log s_j - sum p d log s).  An
+// expert named twice gets both parts, in slot order; an id outside [0, E)
+// takes no part.  One write of each row, and its read only for raw softmax.
+template <int PER, typename Tin>
+__global__ void __launch_bounds__(WARPS * 32) gate_backward(const Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x * (int64_t)WARPS + warp;
+  if (t >= a.T) return;
+  const int E = a.E, k = a.k, e0 = lane * PER;
+  const Tin* row = static_cast<const Tin*>(a.logits) + t * E;
+  int e = -1;
+  float dw = 0.f, lj = -INFINITY;
+  if (lane < k) {
+    e = a.idx[t * k + lane];
+    if (e >= 0 && e < E) {
+      dw = a.dw[t * k + lane];
+      lj = clean(to_f32(row[e]));
+    } else {
+      e = -1;
+    }
+  }
+  float out[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) out[i] = 0.f;
+  float d;
+  if (a.norm) {
+    const float p = share(lj, a.softmax != 0);
+    const float mean = warp_sum(e >= 0 ? p * dw : 0.f);
+    d = a.alpha * p * (dw - mean);
+    if (!a.softmax) d *= sigmoid(-lj);
+  } else if (!a.softmax) {
+    d = a.alpha * dw * sigmoid(lj) * sigmoid(-lj);
+  } else {
+    float l[PER];
+    load_row<PER>(row, E, lane, l);
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
+    float top = warp_max(m);
+    if (top == -INFINITY) top = 0.f;
+    float p = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      out[i] = expf(l[i] - top);
+      p += out[i];
+    }
+    float z = warp_sum(p);
+    if (z == 0.f) z = 1.f;
+    const float s = expf(lj - top) / z;
+    const float sum = warp_sum(e >= 0 ? s * dw : 0.f);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) out[i] = -a.alpha * (out[i] / z) * sum;
+    d = a.alpha * s * dw;
+  }
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl_sync(FULL, e, j);
+    const float dj = __shfl_sync(FULL, d, j);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i == ej) out[i] += dj;
+  }
+  store_row<PER>(static_cast<Tin*>(a.dlogits) + t * E, E, lane, out);
+}
+
+}  // namespace gate
+}  // namespace nh

@@ -1,0 +1,361 @@
+// gemm_f8.cuh -- block-scaled FP8 product on CTA pairs (tcgen05 cta_group::2,
+// kind::f8f6f4): the prefill form of the FP8 experts, shared expert and linear
+// layer.
+//
+//   acc[r, n] = sum_b sx[r, b] sw[n / 128, b] (xq[r] . wq[n] over K block b of 128)
+//
+// The two scales change with every K block, so the product of a block cannot
+// stay in the tensor-memory accumulator: each block is one accumulator (four
+// MMAs of K = 32 starting from zero), two accumulators take turns, and eight
+// epilogue warps per CTA drain one into registers, times its scales, while the
+// tensor cores fill the other.  A tile is 256 rows x 256 features for a pair of
+// CTAs (each stages 128 rows of both operands), so per K block a CTA's warps
+// read 128 x 256 values and do one multiply-add each: a thread owns one row and
+// 128 features, which makes the scale one number per thread and block, keeps
+// the running sum in 128 registers, and leaves the maximum of a (row, 128)
+// block of the output inside one thread, where the next projection's
+// quantization needs it.
+//
+// Roles (384 threads): warp 0 lane 0 TMA producer (both CTAs); warp 1 tensor
+// memory owner, lane 0 of the leader issues the MMAs; warps 4..11 drain (warp
+// w: row quarter w mod 4, feature half (w - 4) / 4).  The first four warps hand
+// registers to the other eight, whose sums would spill in an even split.  Tiles are dealt out in
+// turn (tile i to pair i mod pairs): they all take the same time.  Both CTAs'
+// copies complete on the leader's stage barrier, MMA completion is committed
+// to both CTAs, the peer's drains arrive on the leader's barriers.  Every wait
+// is bounded, as in the bf16 kernels.
+#pragma once
+
+#include "gemm_tc.cuh"
+#include "quant_f8.cuh"
+
+namespace nh {
+namespace f8g {
+
+constexpr int BK = 128;        // K of a stage: one block of scales, one 128-byte row
+constexpr int UMMA_K = 32;
+constexpr int MP = 256, NT = 256, HALF = 128;
+constexpr int STAGES = 6;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr int REGS_ROLES = 48, REGS_DRAIN = 224;   // per thread, after the split
+constexpr int REGS_NEEDED = 128 * REGS_ROLES + 32 * EPI_WARPS * REGS_DRAIN;
+constexpr int OP_BYTES = HALF * BK;
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int TMEM_COLS = 2 * NT;
+constexpr int NBAR = 2 * STAGES + 5;
+constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + NBAR * 8 + 16;
+
+enum Out : int {
+  OUT_BF16 = 0,        // out bf16 [rows, N] = acc
+  OUT_F32 = 1,         // out f32 [rows, N] = acc
+  OUT_RELU2_F8 = 2,    // out E4M3 [rows, N] of relu(acc)^2, scales [rows, ceil(N / 128)]
+  OUT_ADD_F32 = 3,     // out f32 [rows, N] += acc, atomic adds
+  OUT_COMBINE = 4,     // out f32: out[dst_row[r]] += perm_w[r] * acc, atomic adds
+};
+
+struct Args {
+  const float* xs;         // [rows, KB]
+  const float* ws;         // [E, ceil(N / 128), KB]
+  const int4* tiles;       // (expert, first row, rows <= 256, -) or null: dense rows
+  const int32_t* num_tiles;
+  int dense_rows;
+  int N, K, KB;
+  void* out;
+  float* out_scales;       // OUT_RELU2_F8
+  int64_t ldo;
+  const float* perm_w;
+  const int32_t* dst_row;
+  int* status;
+  uint64_t timeout_ns;
+};
+
+// D (+)= A B^T over both CTAs' shared memory, E4M3 in, f32 accumulate, M = 256
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D f32, A and B E4M3 (format 0), both K-major
+__device__ __forceinline__ uint32_t make_idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// 32 accumulator columns of this thread's row: load and wait as one statement,
+// so that nothing that uses the values can move between the two
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ int4 entry(const Args& g, int m) {
+  if (g.tiles) return g.tiles[m];
+  return make_int4(0, m * MP, min(MP, g.dense_rows - m * MP), 0);
+}
+
+// MMA N of a tile with n_eff features left: whole multiples of 32 (weight rows
+// past N arrive as zeros and their columns are not stored)
+__device__ __forceinline__ int mma_n(int n_eff) { return (n_eff + 31) & ~31; }
+
+// One row's 128 features of the tile at its end.  n: how many of them exist
+// (a multiple of 16).
+template <int OUT>
+__device__ __forceinline__ void finish_row(const Args& g, int row, int f0, int n,
+                                           const float (&acc)[128]) {
+  if constexpr (OUT == OUT_BF16) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) +
+                                          (size_t)row * g.ldo + f0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (8 * i < n)
+        dst[i] = make_uint4(pack_bf16x2(acc[8 * i], acc[8 * i + 1]),
+                            pack_bf16x2(acc[8 * i + 2], acc[8 * i + 3]),
+                            pack_bf16x2(acc[8 * i + 4], acc[8 * i + 5]),
+                            pack_bf16x2(acc[8 * i + 6], acc[8 * i + 7]));
+  } else if constexpr (OUT == OUT_F32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(g.out) + (size_t)row * g.ldo + f0);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (4 * i < n)
+        dst[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+  } else if constexpr (OUT == OUT_RELU2_F8) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 128; ++i) {
+      const uint32_t b = f8::mag_bits(f8::relu2_nan(acc[i]));
+      m = max(m, b < f8::INF_BITS && i < n ? b : 0u);
+    }
+    const int e = f8::scale_exp(m);
+    const float inv = f8::pow2(-e);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.out) + (size_t)row * g.ldo + f0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = f8::relu2_nan(acc[16 * i + j]);
+      if (16 * i < n) dst[i] = f8::encode16(v, inv);
+    }
+    g.out_scales[(size_t)row * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
+  } else {
+    const float w = OUT == OUT_COMBINE ? g.perm_w[row] : 1.f;
+    const int64_t to = OUT == OUT_COMBINE ? g.dst_row[row] : row;
+    float* dst = static_cast<float*>(g.out) + to * g.ldo + f0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (4 * i < n)
+        red_add_f32x4(dst + 4 * i, w * acc[4 * i], w * acc[4 * i + 1], w * acc[4 * i + 2],
+                      w * acc[4 * i + 3]);
+  }
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(THREADS, 1)
+    f8_pair_gemm(const __grid_constant__ CUtensorMap map_x,
+                 const __grid_constant__ CUtensorMap map_w, const Args g) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const uint32_t bar0 = base + STAGES * STAGE_BYTES;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + STAGES * STAGE_BYTES + NBAR * 8);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // both CTAs' epilogue warps
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // the peer's barriers are initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  const WaitCtl wc{abort_flag, g.status, g.timeout_ns};
+
+  const int num_m = g.tiles ? *g.num_tiles : (g.dense_rows + MP - 1) / MP;
+  const int n_blocks = (g.N + NT - 1) / NT;
+  const int64_t total = (int64_t)num_m * n_blocks;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int nk = g.KB;
+
+  // the split draws on what the block was launched with: the host checks that
+  // the kernel's registers cover REGS_NEEDED before any launch
+  if (warp < 4) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ROLES));
+   if (warp == 0 && lane == 0) {
+    // ---------------- producer ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    long issued = 0;
+    bool ok = true;
+    for (int64_t tile = pair; ok && tile < total; tile += pairs) {
+      const int m = (int)(tile / n_blocks), nb = (int)(tile - (int64_t)m * n_blocks);
+      const int4 ent = entry(g, m);
+      const int x_row = ent.y + (int)rank * HALF;
+      const int w_row = nb * NT + (int)rank * (mma_n(min(NT, g.N - nb * NT)) / 2);
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!mbar_wait_spin(empty_bar(stage), phase ^ 1u, wc, SITE_TC_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sx = base + stage * STAGE_BYTES, sw = sx + OP_BYTES;
+        const uint32_t fb = map_to_rank(full_bar(stage), 0);
+        if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * STAGE_BYTES);
+        tma_load_2d_pair(sx, &map_x, fb, kb * BK, x_row);
+        tma_load_3d_pair(sw, &map_w, fb, kb * BK, w_row, ent.x);
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && leader) {
+      // the leader's stage barriers count both CTAs' copies: wait for those in flight
+      const long first = issued > STAGES ? issued - STAGES : 0;
+      for (long i = first; i < issued; ++i)
+        tc::mbar_drain(full_bar((int)(i % STAGES)), (uint32_t)((i / STAGES) & 1), g.timeout_ns,
+                       g.status);
+    }
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ---------------- MMA issuer ----------------
+    int stage = 0;
+    uint32_t phase = 0, use = 0;
+    bool ok = true, any = false;
+    for (int64_t tile = pair; ok && tile < total; tile += pairs) {
+      const int nb = (int)(tile % n_blocks);
+      const uint32_t idesc = make_idesc_e4m3(MP, mma_n(min(NT, g.N - nb * NT)));
+      for (int kb = 0; kb < nk; ++kb, ++use) {
+        const uint32_t acc = use & 1u;
+        if (!mbar_wait_cluster(tempty_bar(acc), ((use >> 1) & 1u) ^ 1u, wc, SITE_TC_MMA) ||
+            !mbar_wait_spin(full_bar(stage), phase, wc, SITE_TC_MMA)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sx = base + stage * STAGE_BYTES, sw = sx + OP_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < BK / UMMA_K; ++kk)
+          umma_f8_pair(tmem_base + acc * NT, make_sdesc_sw128(sx + kk * UMMA_K),
+                       make_sdesc_sw128(sw + kk * UMMA_K), idesc, kk != 0);
+        any = true;
+        umma_commit_pair(tfull_bar(acc));
+        umma_commit_pair(map_to_rank(tfull_bar(acc), 1));
+        umma_commit_pair(empty_bar(stage));
+        umma_commit_pair(map_to_rank(empty_bar(stage), 1));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && any) {
+      umma_commit_pair(drain_bar);
+      tc::mbar_drain(drain_bar, 0, g.timeout_ns, g.status);
+    }
+   }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_DRAIN));
+    // ---------------- drain: 32 rows x 128 features per warp ----------------
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
+    uint32_t use = 0;
+    bool ok = true;
+    for (int64_t tile = pair; ok && tile < total; tile += pairs) {
+      const int m = (int)(tile / n_blocks), nb = (int)(tile - (int64_t)m * n_blocks);
+      const int4 ent = entry(g, m);
+      const int f0 = nb * NT + half * 128;
+      const int n = min(128, g.N - f0);            // <= 0: no features in this half
+      const int local = (int)rank * HALF + quarter * 32 + lane;
+      const int row = ent.y + min(local, ent.z - 1);
+      const float* xs = g.xs + (size_t)row * nk;
+      const float* ws = g.ws + ((size_t)ent.x * ((g.N + 127) / 128) + (n > 0 ? f0 / 128 : 0)) * nk;
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      float s = __ldg(xs) * __ldg(ws);
+      for (int kb = 0; kb < nk; ++kb, ++use) {
+        const uint32_t a = use & 1u;
+        int r = 1;
+        if (lane == 0)
+          r = mbar_wait_cluster(tfull_bar(a), (use >> 1) & 1u, wc, SITE_TC_EPILOGUE) ? 1 : 0;
+        r = __shfl_sync(0xffffffffu, r, 0);
+        if (!r) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float s_next = kb + 1 < nk ? __ldg(xs + kb + 1) * __ldg(ws + kb + 1) : 0.f;
+        if (n > 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tq + a * NT + 32u * c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              acc[32 * c + i] = fmaf(s, __uint_as_float(v[i]), acc[32 * c + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            mbar_arrive(tempty_bar(a));
+          else
+            mbar_arrive_cluster(map_to_rank(tempty_bar(a), 0));
+        }
+        s = s_next;
+      }
+      if (ok && n > 0 && local < ent.z) finish_row<OUT>(g, row, f0, n, acc);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // no CTA leaves while its peer may still touch its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+}  // namespace f8g
+}  // namespace nh

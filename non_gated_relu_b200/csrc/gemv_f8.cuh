@@ -1,0 +1,197 @@
+// gemv_f8.cuh -- block-scaled FP8 product for few rows (at most 32 per
+// expert): the decode form of the FP8 experts, shared expert and linear layer.
+//
+//   out[r, n] = epi( sum_b sx[r, b] sw[n / 128, b] (xq[r] . wq[n] over block b) )
+//
+// Bound by the weights' bytes.  A CTA takes 16 weight rows of one tile entry
+// over the whole K and its 8 warps take K blocks of 128 in turn, so the bytes
+// of a task are all asked for at once: lane (g, q) loads 16 bytes of rows g and
+// g + 8 at 16 q of each half block, straight into the fragments of
+// mma.sync m16n8k32 (E4M3, float32 accumulate).  The order of features inside
+// an MMA is free as long as both operands agree, so word i of a lane's 16
+// bytes is k-slot i for weights and activations alike.  Each block's product
+// starts from zero and enters the running sum times its two scales; the warps'
+// sums are added in warp order, so a result does not depend on scheduling.
+#pragma once
+
+#include "gemm_tc.cuh"
+#include "quant_f8.cuh"
+
+namespace nh {
+namespace f8v {
+
+constexpr int WARPS = 8;
+constexpr int MT = 16;      // weight rows of a task
+
+enum Out : int {
+  OUT_BF16 = 0,       // out bf16 [rows, N] = acc
+  OUT_F32 = 1,        // out f32 [rows, N] = acc
+  OUT_RELU2_F32 = 2,  // out f32 [rows, N] = relu(acc)^2   (quantized by the next kernel)
+  OUT_ADD_F32 = 3,    // out f32 [rows, N] += acc, atomic adds
+  OUT_COMBINE = 4,    // out f32: out[dst_row[r]] += perm_w[r] * acc, atomic adds
+};
+
+struct Args {
+  const uint8_t* x;        // codes [rows of x, K]
+  const float* xs;         // scales [rows of x, KB]
+  const uint8_t* w;        // codes [E, N, K]
+  const float* ws;         // scales [E, ceil(N / 128), KB]
+  const int4* tiles;       // (expert, first row, rows, -) or null: dense rows
+  const int32_t* num_tiles;
+  int dense_rows, tile_rows;
+  int N, K, KB;
+  const int32_t* row_token;  // row r reads x row row_token[r]; null: row r
+  int out_kind;
+  void* out;
+  int64_t ldo;
+  const float* perm_w;
+  const int32_t* dst_row;
+  int early_w;             // weights and tile table were complete before the
+                           // previous launch in the stream began its work
+};
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// NT: rows of a tile entry, padded (8, 16, 32); U: K blocks of a warp in flight
+template <int NT, int U>
+__global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
+  constexpr int NB = NT / 8;
+  __shared__ float red[WARPS][MT][NT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gq = lane >> 2, tq = lane & 3;
+  const int n_rb = a.N / MT;
+  const int m = blockIdx.x / n_rb, rb = blockIdx.x - m * n_rb;
+  const int n0 = rb * MT;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+
+  bool waited = false;
+  auto wait_previous = [&]() {
+    pdl_wait();
+    pdl_trigger();
+    waited = true;
+  };
+  if (!a.early_w) wait_previous();
+  int4 ent = make_int4(0, m * a.tile_rows, 0, 0);
+  if (a.tiles != nullptr) {
+    if (m >= *a.num_tiles) {
+      if (!waited) wait_previous();
+      return;
+    }
+    ent = a.tiles[m];
+  } else {
+    ent.z = min(a.tile_rows, a.dense_rows - ent.y);
+  }
+  const uint8_t* w0 = a.w + ((size_t)ent.x * a.N + n0 + gq) * a.K;
+  const uint8_t* w1 = w0 + (size_t)8 * a.K;
+  const float* ws = a.ws + ((size_t)ent.x * ((a.N + 127) / 128) + n0 / 128) * a.KB;
+
+  float acc[NB][4];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+
+  // x rows of this lane's fragment columns (token gq of each n-tile) and of its
+  // accumulator columns (tokens 2 tq, 2 tq + 1); rows past the entry repeat its
+  // last row and are not stored
+  const uint8_t* xp[NB];
+  const float* sp[NB][2];
+  bool have_rows = false;
+
+  for (int b0 = warp; b0 < a.KB; b0 += WARPS * U) {
+    uint4 wv[U][4];
+    float sw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * WARPS;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int off = b * 128 + h * 64 + tq * 16;
+        const bool in = b < a.KB && off < a.K;
+        wv[u][2 * h] = in ? load_stream(w0 + off) : zero;
+        wv[u][2 * h + 1] = in ? load_stream(w1 + off) : zero;
+      }
+      sw[u] = b < a.KB ? __ldg(ws + b) : 0.f;
+    }
+    if (!waited) wait_previous();
+    if (!have_rows) {
+      have_rows = true;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int r = ent.y + min(8 * j + gq, ent.z - 1);
+        const int r0 = ent.y + min(8 * j + 2 * tq, ent.z - 1);
+        const int r1 = ent.y + min(8 * j + 2 * tq + 1, ent.z - 1);
+        xp[j] = a.x + (size_t)(a.row_token ? a.row_token[r] : r) * a.K;
+        sp[j][0] = a.xs + (size_t)(a.row_token ? a.row_token[r0] : r0) * a.KB;
+        sp[j][1] = a.xs + (size_t)(a.row_token ? a.row_token[r1] : r1) * a.KB;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * WARPS;
+      if (b >= a.KB) break;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (8 * j >= ent.z) break;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int off = b * 128 + h * 64 + tq * 16;
+          const uint4 xv = off < a.K ? *reinterpret_cast<const uint4*>(xp[j] + off) : zero;
+          const uint4 p = wv[u][2 * h], q = wv[u][2 * h + 1];
+          mma_e4m3(d, p.x, q.x, p.y, q.y, xv.x, xv.y);
+          mma_e4m3(d, p.z, q.z, p.w, q.w, xv.z, xv.w);
+        }
+        const float s0 = sp[j][0][b] * sw[u], s1 = sp[j][1][b] * sw[u];
+        acc[j][0] = fmaf(s0, d[0], acc[j][0]);
+        acc[j][1] = fmaf(s1, d[1], acc[j][1]);
+        acc[j][2] = fmaf(s0, d[2], acc[j][2]);
+        acc[j][3] = fmaf(s1, d[3], acc[j][3]);
+      }
+    }
+  }
+  if (!waited) wait_previous();   // a warp without a K block
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    red[warp][gq][8 * j + 2 * tq] = acc[j][0];
+    red[warp][gq][8 * j + 2 * tq + 1] = acc[j][1];
+    red[warp][gq + 8][8 * j + 2 * tq] = acc[j][2];
+    red[warp][gq + 8][8 * j + 2 * tq + 1] = acc[j][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * NT; i += WARPS * 32) {
+    const int f = i % MT, c = i / MT;
+    if (c >= ent.z) break;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += red[w][f][c];
+    const int r = ent.y + c;
+    const size_t at = (size_t)r * a.ldo + n0 + f;
+    switch (a.out_kind) {
+      case OUT_BF16: static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v); break;
+      case OUT_F32: static_cast<float*>(a.out)[at] = v; break;
+      case OUT_RELU2_F32: static_cast<float*>(a.out)[at] = f8::relu2_nan(v); break;
+      case OUT_ADD_F32: red_add_f32(static_cast<float*>(a.out) + at, v); break;
+      default:
+        red_add_f32(static_cast<float*>(a.out) + (size_t)a.dst_row[r] * a.ldo + n0 + f,
+                    a.perm_w[r] * v);
+    }
+  }
+}
+
+}  // namespace f8v
+}  // namespace nh

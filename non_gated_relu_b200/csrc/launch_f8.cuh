@@ -1,0 +1,185 @@
+// launch_f8.cuh -- host side of the FP8 operators: tensor maps, kernel choice
+// and launches.  Part of nh_moe.cu (inside namespace nh).
+
+// uint8 [rows, row_bytes], box 128 bytes x 128 rows, 128-byte swizzle
+static nh_status map_u8_2d(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(NH_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)f8g::BK, (cuuint32_t)f8g::HALF};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NH_ERR_CUDA, "cuTensorMapEncodeTiled (u8 2d) failed: %d", (int)r);
+  return NH_OK;
+}
+
+static nh_status check_f8(const nh_fp8_weight* w, const char* name) {
+  if (!w) return fail(NH_ERR_INVALID_ARG, "%s is NULL", name);
+  NH_TRY(check_ptr(w->codes, name));
+  return check_ptr(w->scales, name);
+}
+
+// One product: out = outkind(x W[e]^T) over tile entries or dense rows.
+enum F8Out { F8_BF16, F8_F32, F8_RELU2, F8_ADD, F8_COMBINE };
+struct F8Call {
+  const uint8_t* x;          // codes [x_rows, K]
+  const float* xs;
+  int64_t x_rows;
+  const nh_fp8_weight* w;    // [n_exp, N, K]
+  int n_exp;
+  int64_t rows;              // output rows
+  int N, K;
+  const int4* tiles;
+  const int32_t* num_tiles;
+  int max_tiles;
+  int tile_rows;
+  bool gemv;
+  F8Out out_kind;
+  void* out;                 // F8_RELU2: codes (pair GEMM) or float32 (GEMV)
+  float* out_scales;         // F8_RELU2 of the pair GEMM
+  const int32_t* row_token;
+  const float* perm_w;
+  const int32_t* dst_row;
+  int* status;
+  bool early_w;
+};
+
+static nh_status launch_f8_gemv(const F8Call& c, cudaStream_t st) {
+  f8v::Args a{};
+  a.x = c.x;
+  a.xs = c.xs;
+  a.w = c.w->codes;
+  a.ws = c.w->scales;
+  a.tiles = c.tiles;
+  a.num_tiles = c.num_tiles;
+  a.dense_rows = (int)c.rows;
+  a.tile_rows = c.tile_rows;
+  a.N = c.N;
+  a.K = c.K;
+  a.KB = (int)f8_blocks(c.K);
+  a.row_token = c.row_token;
+  switch (c.out_kind) {
+    case F8_BF16: a.out_kind = f8v::OUT_BF16; break;
+    case F8_F32: a.out_kind = f8v::OUT_F32; break;
+    case F8_RELU2: a.out_kind = f8v::OUT_RELU2_F32; break;
+    case F8_ADD: a.out_kind = f8v::OUT_ADD_F32; break;
+    default: a.out_kind = f8v::OUT_COMBINE;
+  }
+  a.out = c.out;
+  a.ldo = c.N;
+  a.perm_w = c.perm_w;
+  a.dst_row = c.dst_row;
+  a.early_w = c.early_w ? 1 : 0;
+  // an entry holds at least one row
+  const int64_t m = c.tiles ? std::min<int64_t>(c.max_tiles, c.rows)
+                            : (c.rows + c.tile_rows - 1) / c.tile_rows;
+  const int64_t grid = m * (c.N / f8v::MT);
+  if (grid <= 0) return NH_OK;
+  if (grid > 0x7fffffff) return fail(NH_ERR_UNSUPPORTED, "FP8 GEMV: %lld tasks", (long long)grid);
+  const dim3 g((unsigned)grid), b(f8v::WARPS * 32);
+  switch (c.tile_rows) {
+    case 8: return launch_k("f8_gemv", f8v::f8_gemv<8, 3>, g, b, 0, st, a);
+    case 16: return launch_k("f8_gemv", f8v::f8_gemv<16, 2>, g, b, 0, st, a);
+    case 32: return launch_k("f8_gemv", f8v::f8_gemv<32, 2>, g, b, 0, st, a);
+    default: return fail(NH_ERR_UNSUPPORTED, "FP8 GEMV rows %d", c.tile_rows);
+  }
+}
+
+template <int OUT>
+static nh_status launch_f8_pair_as(const F8Call& c, const f8g::Args& a, int64_t tiles, int dev,
+                                   cudaStream_t st) {
+  CUtensorMap mx, mw;
+  NH_TRY(map_u8_2d(&mx, c.x, c.K, c.x_rows));
+  NH_TRY(map_u8_3d(&mw, c.w->codes, c.K, c.N, c.n_exp, f8g::BK, true));
+  const int64_t pairs = std::min<int64_t>(tiles, g_f8_clusters[dev]);
+  if (pairs <= 0) return NH_OK;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+  lc.blockDim = dim3(f8g::THREADS, 1, 1);
+  lc.dynamicSmemBytes = f8g::SMEM;
+  lc.stream = st;
+  cudaLaunchAttribute at[3];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  at[2].id = cudaLaunchAttributePriority;
+  at[2].val.priority = stream_priority(st);
+  lc.attrs = at;
+  lc.numAttrs = 3;
+  NH_CUDA(cudaLaunchKernelEx(&lc, f8g::f8_pair_gemm<OUT>, mx, mw, a));
+  return launch_check("f8_pair_gemm");
+}
+
+static nh_status launch_f8_pair(const F8Call& c, int dev, cudaStream_t st) {
+  f8g::Args a{};
+  a.xs = c.xs;
+  a.ws = c.w->scales;
+  a.tiles = c.tiles;
+  a.num_tiles = c.num_tiles;
+  a.dense_rows = (int)c.rows;
+  a.N = c.N;
+  a.K = c.K;
+  a.KB = (int)f8_blocks(c.K);
+  a.out = c.out;
+  a.out_scales = c.out_scales;
+  a.ldo = c.N;
+  a.perm_w = c.perm_w;
+  a.dst_row = c.dst_row;
+  a.status = c.status;
+  a.timeout_ns = timeout_ns();
+  const int64_t m = c.tiles ? c.max_tiles : (c.rows + f8g::MP - 1) / f8g::MP;
+  const int64_t tiles = m * ((c.N + f8g::NT - 1) / f8g::NT);
+  switch (c.out_kind) {
+    case F8_BF16: return launch_f8_pair_as<f8g::OUT_BF16>(c, a, tiles, dev, st);
+    case F8_F32: return launch_f8_pair_as<f8g::OUT_F32>(c, a, tiles, dev, st);
+    case F8_RELU2: return launch_f8_pair_as<f8g::OUT_RELU2_F8>(c, a, tiles, dev, st);
+    case F8_ADD: return launch_f8_pair_as<f8g::OUT_ADD_F32>(c, a, tiles, dev, st);
+    default: return launch_f8_pair_as<f8g::OUT_COMBINE>(c, a, tiles, dev, st);
+  }
+}
+
+static nh_status run_f8(const F8Call& c, int dev, cudaStream_t st) {
+  if (c.rows == 0) return NH_OK;
+  return c.gemv ? launch_f8_gemv(c, st) : launch_f8_pair(c, dev, st);
+}
+
+// Quantize R rows of C values; with inv_row each to its k permuted rows.
+template <typename Tin>
+static nh_status launch_quantize(const Tin* x, int64_t R, int C, uint8_t* codes, float* scales,
+                                 const int32_t* inv_row, int k, int dev, cudaStream_t st) {
+  const int64_t kb = f8_blocks(C), units = R * kb;
+  if (units == 0) return NH_OK;
+  if (units > 0x7fffffff) return fail(NH_ERR_UNSUPPORTED, "quantization of %lld blocks", (long long)units);
+  return launch_k("quantize_rows", f8::quantize_rows<Tin>, dim3(grid_for(units, 32, dev)), dim3(256),
+                  0, st, x, (uint32_t)units, C, (int)kb, codes, scales, inv_row, k);
+}
+
+// Dense rows that a kernel left in float32 behind their quantized form
+// (f8_hidden_bytes): where the GEMV writes its squared relu, or codes directly
+struct F8Hidden {
+  uint8_t* codes;
+  float* scales;
+  float* f32;
+};
+static F8Hidden f8_hidden(void* base, int64_t R, int64_t C) {
+  char* b = static_cast<char*>(base);
+  return {reinterpret_cast<uint8_t*>(b), reinterpret_cast<float*>(b + f8_scales_at(R, C)),
+          reinterpret_cast<float*>(b + f8_rows_bytes(R, C))};
+}
+
+// up projection with relu^2, its result quantized: c.out and c.out_scales are
+// set here from `h`
+static nh_status run_f8_up(F8Call c, const F8Hidden& h, int dev, cudaStream_t st) {
+  c.out_kind = F8_RELU2;
+  c.out = c.gemv ? static_cast<void*>(h.f32) : h.codes;
+  c.out_scales = h.scales;
+  NH_TRY(run_f8(c, dev, st));
+  if (!c.gemv) return NH_OK;
+  return launch_quantize(h.f32, c.rows, c.N, h.codes, h.scales, nullptr, 0, dev, st);
+}

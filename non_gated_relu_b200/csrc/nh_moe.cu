@@ -18,6 +18,9 @@
 #include "gemm_q4.cuh"
 #include "gemv_q4.cuh"
 #include "gemv_bf16.cuh"
+#include "gemm_f8.cuh"
+#include "gemv_f8.cuh"
+#include "gate.cuh"
 #include "permute.cuh"
 #include "route.cuh"
 #include "route_permute.cuh"
@@ -78,7 +81,23 @@ constexpr int ROUTE_PERMUTE_MAX_E = 256;
 // fused decode router + permute: 8 warps x 2E selection floats + E + 3 T k
 constexpr int ROUTE_PERMUTE_SMEM_MAX = (16 * 256 + 256 + 3 * 32 * 32) * 4;
 
+constexpr int F8_GEMV_ROWS = 32;   // rows up to which the FP8 products run as GEMVs
+
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+// scale blocks of 128 features
+static int64_t f8_blocks(int64_t n) { return (n + f8::BLK - 1) / f8::BLK; }
+
+// Quantized rows [R, C] in a workspace: codes, then (256-byte aligned) scales
+static size_t f8_scales_at(int64_t R, int64_t C) { return align_up((size_t)R * C, ALIGN); }
+static size_t f8_rows_bytes(int64_t R, int64_t C) {
+  return f8_scales_at(R, C) + align_up((size_t)R * f8_blocks(C) * 4, ALIGN);
+}
+// The experts' hidden rows: quantized, and behind them in float32 where a GEMV
+// wrote them before their quantization
+static size_t f8_hidden_bytes(int64_t R, int64_t C, bool gemv) {
+  return f8_rows_bytes(R, C) + (gemv ? (size_t)R * C * 4 : 0);
+}
 
 static nh_status validate(const nh_moe_config* c) {
   if (!c) return fail(NH_ERR_INVALID_ARG, "cfg is NULL");
@@ -106,10 +125,13 @@ static nh_status validate(const nh_moe_config* c) {
     return fail(NH_ERR_INVALID_ARG, "unknown group_score");
   if (c->group_score == NH_GROUP_SCORE_TOP2 && g < 2)
     return fail(NH_ERR_INVALID_ARG, "the top-2 group score needs >= 2 experts per group");
-  if (c->weight_format != NH_WEIGHTS_NATIVE && c->weight_format != NH_WEIGHTS_NVFP4)
+  if (c->weight_format != NH_WEIGHTS_NATIVE && c->weight_format != NH_WEIGHTS_NVFP4 &&
+      c->weight_format != NH_WEIGHTS_FP8)
     return fail(NH_ERR_INVALID_ARG, "unknown weight_format");
   if (c->weight_format == NH_WEIGHTS_NVFP4 && c->dtype != NH_BF16)
     return fail(NH_ERR_INVALID_ARG, "NVFP4 weights need bf16 activations (W4A16)");
+  if (c->weight_format == NH_WEIGHTS_FP8 && c->dtype != NH_BF16)
+    return fail(NH_ERR_INVALID_ARG, "FP8 weights need bf16 activations");
   if (c->latent_size < 0) return fail(NH_ERR_INVALID_ARG, "latent_size must be >= 0");
   // valid; now what the kernels implement
   if (c->n_routed_experts > MAX_E)
@@ -142,6 +164,10 @@ static void tile_plan(const nh_moe_config* c, int64_t T, int* tile_rows, int* sw
     // weights are dequantized per stage: always weights on the MMA M side
     *tile_rows = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
     *swap = 1;
+  } else if (c->weight_format == NH_WEIGHTS_FP8) {
+    // up to F8_GEMV_ROWS tokens: weight rows on the MMA M side, 8 tokens on N
+    *tile_rows = T <= 8 ? 8 : (T <= 16 ? 16 : (T <= F8_GEMV_ROWS ? F8_GEMV_ROWS : f8g::MP));
+    *swap = T <= F8_GEMV_ROWS ? 1 : 0;
   } else if (c->dtype == NH_F32) {
     *tile_rows = SG_BM;
     *swap = 0;
@@ -203,8 +229,14 @@ static nh_status make_plan(const nh_moe_config* c, int64_t T, Plan* p) {
   L.inv_row = take((size_t)rows * 4);
   L.tiles = take((size_t)L.max_tiles * 16);
   L.num_tiles = take(4);
-  L.x_perm = take(L.x_direct ? 0 : (size_t)rows * p->H * p->elem);
-  L.h = take((size_t)rows * p->I * p->elem);
+  if (c->weight_format == NH_WEIGHTS_FP8) {
+    L.x_direct = sw;   // GEMV: the up projection reads the tokens' rows of x (quantized)
+    L.x_perm = take(f8_rows_bytes(sw ? T : rows, p->H));
+    L.h = take(f8_hidden_bytes(rows, p->I, sw != 0));
+  } else {
+    L.x_perm = take(L.x_direct ? 0 : (size_t)rows * p->H * p->elem);
+    L.h = take((size_t)rows * p->I * p->elem);
+  }
   L.ready = take((size_t)L.max_tiles * 4);
   L.total_bytes = o;
   return NH_OK;
@@ -226,6 +258,13 @@ static nh_status check_ws(const Plan& p, void* ws, size_t ws_bytes) {
   return NH_OK;
 }
 
+// FP8 weights have their own entry points
+static nh_status no_fp8(const nh_moe_config* c, const char* what) {
+  if (c && c->weight_format == NH_WEIGHTS_FP8)
+    return fail(NH_ERR_INVALID_ARG, "%s: config has FP8 weights: use the _fp8 entry points", what);
+  return NH_OK;
+}
+
 // the routed-expert calls take the expert-width config of a latent block
 static nh_status no_latent(const nh_moe_config* c, const char* what) {
   if (c && c->latent_size)
@@ -240,9 +279,16 @@ static T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-static PermuteOut permute_out(void* ws, const nh_moe_ws_layout& L, int* status) {
+static int tile_attach(const nh_moe_config* c, const nh_moe_ws_layout& L) {
+  return c->weight_format == NH_WEIGHTS_NATIVE && L.tile_rows == PAIR_TILE_ROWS ? PAIR_ATTACH_ROWS
+                                                                              : 0;
+}
+
+static PermuteOut permute_out(const nh_moe_config* c, void* ws, const nh_moe_ws_layout& L,
+                              int* status) {
   PermuteOut o;
   o.tile_rows = L.tile_rows;
+  o.attach = tile_attach(c, L);
   o.max_tiles = L.max_tiles;
   o.counts = at<int32_t>(ws, L.counts);
   o.offsets = at<int32_t>(ws, L.offsets);
@@ -254,7 +300,8 @@ static PermuteOut permute_out(void* ws, const nh_moe_ws_layout& L, int* status) 
   o.x_perm = at<void>(ws, L.x_perm);
   o.status = status;
   o.sched_zero = reinterpret_cast<unsigned int*>(status + SCHED_UP);
-  o.gather = L.x_direct ? 0 : 1;
+  // FP8: the rows are gathered as they are quantized, by the up projection's call
+  o.gather = L.x_direct || c->weight_format == NH_WEIGHTS_FP8 ? 0 : 1;
   o.ready = at<int>(ws, L.ready);
   o.n_ready = L.max_tiles;
   return o;
@@ -267,6 +314,7 @@ constexpr int MAX_DEVICES = 64;
 static std::once_flag g_attr_once[MAX_DEVICES];
 static int g_sm_count[MAX_DEVICES];
 static int g_pair_clusters[MAX_DEVICES];  // co-resident 2-CTA clusters of tc2_grouped_gemm
+static int g_f8_clusters[MAX_DEVICES];    // and of f8_pair_gemm
 static nh_status g_attr_status[MAX_DEVICES];
 
 using TcPrefill = tc::Shape<false, 256, 4>;
@@ -274,6 +322,18 @@ using TcPrefill128 = tc::Shape<false, 128, 6>;
 using TcSwap16 = tc::Shape<true, 16, 8>;
 using TcSwap32 = tc::Shape<true, 32, 8>;
 using TcSwap64 = tc::Shape<true, 64, 6>;
+
+// Shared memory of one FP8 pair GEMM; its warps move registers between them
+// (setmaxnreg), which waits for good unless the launch brought enough.
+template <typename Kern>
+static nh_status f8_pair_attrs(Kern kernel) {
+  NH_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, f8g::SMEM));
+  cudaFuncAttributes fa;
+  NH_CUDA(cudaFuncGetAttributes(&fa, kernel));
+  if (fa.numRegs * f8g::THREADS < f8g::REGS_NEEDED)
+    return fail(NH_ERR_UNSUPPORTED, "f8_pair_gemm was built with %d registers a thread", fa.numRegs);
+  return NH_OK;
+}
 
 static nh_status set_attrs(int dev) {
   cudaDeviceProp prop;
@@ -304,6 +364,11 @@ static nh_status set_attrs(int dev) {
                                cudaFuncAttributeMaxDynamicSharedMemorySize, ROUTE_PERMUTE_SMEM_MAX));
   NH_CUDA(cudaFuncSetAttribute(route_permute_small<float>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, ROUTE_PERMUTE_SMEM_MAX));
+  NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_BF16>));
+  NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_F32>));
+  NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_RELU2_F8>));
+  NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_ADD_F32>));
+  NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_COMBINE>));
   {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(2 * (prop.multiProcessorCount / 2), 1, 1);
@@ -320,6 +385,11 @@ static nh_status set_attrs(int dev) {
     NH_CUDA(cudaOccupancyMaxActiveClusters(&n, tc2::tc2_grouped_gemm, &lc));
     if (n < 1) return fail(NH_ERR_UNSUPPORTED, "no 2-CTA cluster of the pair GEMM fits on device %d", dev);
     g_pair_clusters[dev] = n;
+    lc.blockDim = dim3(f8g::THREADS, 1, 1);
+    lc.dynamicSmemBytes = f8g::SMEM;
+    NH_CUDA(cudaOccupancyMaxActiveClusters(&n, f8g::f8_pair_gemm<f8g::OUT_COMBINE>, &lc));
+    if (n < 1) return fail(NH_ERR_UNSUPPORTED, "no 2-CTA cluster of the FP8 GEMM fits on device %d", dev);
+    g_f8_clusters[dev] = n;
   }
   return NH_OK;
 }
@@ -880,6 +950,9 @@ static int grid_for(int64_t n, int per_block, int dev) {
   return (int)(b < 1 ? 1 : b);
 }
 
+#include "launch_f8.cuh"
+#include "launch_gate.cuh"
+
 }  // namespace nh
 
 using namespace nh;
@@ -916,7 +989,57 @@ nh_status nh_moe_shared_workspace_size(const nh_moe_config* cfg, int64_t T, size
   Plan p;
   NH_TRY(make_plan(cfg, T, &p));
   if (!cfg->n_shared_experts) return fail(NH_ERR_INVALID_ARG, "config has no shared expert");
-  *bytes = ALIGN + align_up((size_t)T * p.S * p.elem + 1, ALIGN);
+  if (cfg->weight_format == NH_WEIGHTS_FP8)
+    *bytes = ALIGN + f8_rows_bytes(T, p.H) + f8_hidden_bytes(T, p.S, p.lay.swap_ab != 0);
+  else
+    *bytes = ALIGN + align_up((size_t)T * p.S * p.elem + 1, ALIGN);
+  return NH_OK;
+}
+
+// logits [T, E] of more than 32 tokens into the workspace
+static nh_status route_logits(const Plan& p, int64_t T, const void* x, const float* w_router,
+                              void* ws, int dev, cudaStream_t st) {
+  int* status = at<int>(ws, p.lay.status);
+  float* logits = at<float>(ws, p.lay.logits);
+  if (p.bf16 && p.E % 32 == 0) {
+    // logits on the tensor cores: x (bf16) against the fp32 router weight split
+    // into three bf16 planes, accumulated over K = 3H in fp32
+    __nv_bfloat16* wsplit = at<__nv_bfloat16>(ws, p.lay.router_w);
+    NH_TRY((launch_k("router_split", router_split, dim3(grid_for((int64_t)p.E * p.H, 256, dev)), dim3(256), 0, st, w_router, wsplit, p.E,
+                                                                          p.H)));
+    NH_TRY(launch_check("router_split"));
+    GemmCall c{};
+    c.A = x;
+    c.a_kwrap = p.H;
+    c.rows = T;
+    c.W = wsplit;
+    c.n_exp = 1;
+    c.N = p.E;
+    c.K = 3 * p.H;
+    c.tiles = nullptr;
+    c.tile_rows = tc::M;
+    c.swap = 0;
+    c.epi = EPI_STORE_F32;
+    c.out = logits;
+    c.ldo = p.E;
+    c.status = status;
+    c.sched = reinterpret_cast<unsigned int*>(status + SCHED_ROUTER);
+    // up to 128 experts fit one 128-wide N tile (a 256-wide tile would spend
+    // half of its MMA work on zero-filled weight rows)
+    if (p.E <= 128)
+      NH_TRY((launch_tc<false, 128, 6>(c, dev, st)));
+    else
+      NH_TRY((launch_tc<false, 256, 4>(c, dev, st)));
+  } else {
+    dim3 grid((unsigned)((T + RT_BT - 1) / RT_BT), (unsigned)((p.E + RT_BE - 1) / RT_BE));
+    if (p.bf16)
+      NH_TRY((launch_k("router_logits_tiled", router_logits_tiled<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, 
+          static_cast<const __nv_bfloat16*>(x), w_router, logits, (int)T, p.H, p.E)));
+    else
+      NH_TRY((launch_k("router_logits_tiled", router_logits_tiled<float>, dim3(grid), dim3(256), 0, st, static_cast<const float*>(x), w_router,
+                                                       logits, (int)T, p.H, p.E)));
+    NH_TRY(launch_check("router_logits_tiled"));
+  }
   return NH_OK;
 }
 
@@ -972,45 +1095,7 @@ nh_status nh_moe_route(const nh_moe_config* cfg, int64_t T, const void* x, const
                                                                 w_router, a, p.H, done)));
     return launch_check("router_fused_small");
   }
-  if (p.bf16 && p.E % 32 == 0) {
-    // logits on the tensor cores: x (bf16) against the fp32 router weight split
-    // into three bf16 planes, accumulated over K = 3H in fp32
-    __nv_bfloat16* wsplit = at<__nv_bfloat16>(ws, p.lay.router_w);
-    NH_TRY((launch_k("router_split", router_split, dim3(grid_for((int64_t)p.E * p.H, 256, dev)), dim3(256), 0, st, w_router, wsplit, p.E,
-                                                                          p.H)));
-    NH_TRY(launch_check("router_split"));
-    GemmCall c{};
-    c.A = x;
-    c.a_kwrap = p.H;
-    c.rows = T;
-    c.W = wsplit;
-    c.n_exp = 1;
-    c.N = p.E;
-    c.K = 3 * p.H;
-    c.tiles = nullptr;
-    c.tile_rows = tc::M;
-    c.swap = 0;
-    c.epi = EPI_STORE_F32;
-    c.out = logits;
-    c.ldo = p.E;
-    c.status = status;
-    c.sched = reinterpret_cast<unsigned int*>(status + SCHED_ROUTER);
-    // up to 128 experts fit one 128-wide N tile (a 256-wide tile would spend
-    // half of its MMA work on zero-filled weight rows)
-    if (p.E <= 128)
-      NH_TRY((launch_tc<false, 128, 6>(c, dev, st)));
-    else
-      NH_TRY((launch_tc<false, 256, 4>(c, dev, st)));
-  } else {
-    dim3 grid((unsigned)((T + RT_BT - 1) / RT_BT), (unsigned)((p.E + RT_BE - 1) / RT_BE));
-    if (p.bf16)
-      NH_TRY((launch_k("router_logits_tiled", router_logits_tiled<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, 
-          static_cast<const __nv_bfloat16*>(x), w_router, logits, (int)T, p.H, p.E)));
-    else
-      NH_TRY((launch_k("router_logits_tiled", router_logits_tiled<float>, dim3(grid), dim3(256), 0, st, static_cast<const float*>(x), w_router,
-                                                       logits, (int)T, p.H, p.E)));
-    NH_TRY(launch_check("router_logits_tiled"));
-  }
+  NH_TRY(route_logits(p, T, x, w_router, ws, dev, st));
   NH_TRY((launch_k("router_select", router_select, dim3((unsigned)((T + 7) / 8)), dim3(256), sel_smem, st, a)));
   return launch_check("router_select");
 }
@@ -1094,7 +1179,7 @@ nh_status nh_moe_permute(const nh_moe_config* cfg, int64_t T, const void* x,
   int* status = at<int>(ws, L.status);
   if (T <= PERM_CHUNK) {
     // decode-sized: the whole permute in one block
-    const PermuteOut o = permute_out(ws, L, status);
+    const PermuteOut o = permute_out(cfg, ws, L, status);
     const size_t smem = (size_t)(p.E + T * p.k) * sizeof(int);
     if (p.bf16)
       NH_TRY((launch_k("permute_small", permute_small<__nv_bfloat16>, dim3(1), dim3(512), smem, st,
@@ -1110,6 +1195,7 @@ nh_status nh_moe_permute(const nh_moe_config* cfg, int64_t T, const void* x,
   NH_TRY(launch_check("permute_hist"));
   const int scan_threads = ((p.E + 31) / 32) * 32;
   NH_TRY((launch_k("permute_scan", permute_scan, dim3(1), dim3(scan_threads), 0, st, chunk, L.n_chunks, p.E, L.tile_rows,
+                                            tile_attach(cfg, L),
                                             at<int32_t>(ws, L.counts), at<int32_t>(ws, L.offsets),
                                             at<int4>(ws, L.tiles), at<int32_t>(ws, L.num_tiles),
                                             L.max_tiles,
@@ -1123,6 +1209,7 @@ nh_status nh_moe_permute(const nh_moe_config* cfg, int64_t T, const void* x,
         at<int32_t>(ws, L.perm_token), at<float>(ws, L.perm_w), at<int32_t>(ws, L.inv_row),
         at<__nv_bfloat16>(ws, L.x_perm), status, 0)));
     NH_TRY(launch_check("permute_scatter"));
+    if (cfg->weight_format == NH_WEIGHTS_FP8) return NH_OK;
     NH_TRY((launch_k("permute_gather", permute_gather<__nv_bfloat16>, dim3(gather_blocks), dim3(256), 0, st, 
         static_cast<const __nv_bfloat16*>(x), at<int32_t>(ws, L.inv_row), (int)T, p.k, p.H,
         at<__nv_bfloat16>(ws, L.x_perm))));
@@ -1177,7 +1264,7 @@ nh_status nh_moe_route_permute(const nh_moe_config* cfg, int64_t T, const void* 
   a.alpha = cfg->routed_scaling_factor;
   a.group_score = cfg->group_score;
   a.use_sigma = (bias != nullptr) || cfg->group_score == NH_GROUP_SCORE_TOP2;
-  const PermuteOut o = permute_out(ws, L, status);
+  const PermuteOut o = permute_out(cfg, ws, L, status);
   const size_t smem = (size_t)(16 * p.E + p.E + 3 * T * p.k) * sizeof(float);
   unsigned int* done = reinterpret_cast<unsigned int*>(status + 3);
   if (p.bf16)
@@ -1239,6 +1326,7 @@ static nh_status experts_phase(const nh_moe_config* cfg, int64_t T, const void* 
                                void* ws, size_t ws_bytes, float* y_acc, void* stream,
                                bool up_phase, const nh_nvfp4_weight* wq = nullptr) {
   NH_TRY(no_latent(cfg, "routed experts"));
+  NH_TRY(no_fp8(cfg, "routed experts"));
   Plan p;
   NH_TRY(make_plan(cfg, T, &p));
   NH_TRY(check_ws(p, ws, ws_bytes));
@@ -1358,6 +1446,7 @@ static nh_status shared_impl(const nh_moe_config* cfg, int64_t T, const void* x,
                              size_t ws_shared_bytes, void* stream, bool store) {
   Plan p;
   NH_TRY(make_plan(cfg, T, &p));
+  NH_TRY(no_fp8(cfg, "nh_moe_shared"));
   const bool nvfp4 = cfg->weight_format == NH_WEIGHTS_NVFP4;
   if (nvfp4 != (q_su != nullptr))
     return fail(NH_ERR_INVALID_ARG, nvfp4 ? "config has NVFP4 weights: use nh_moe_shared_nvfp4"
@@ -1560,5 +1649,8 @@ nh_status nh_moe_selftest_timeout(void* ws, uint64_t timeout, void* stream) {
   selftest_timeout_kernel<<<1, 32, 0, st>>>(static_cast<int*>(ws), timeout);
   return launch_check("selftest_timeout");
 }
+
+#include "api_f8.cuh"
+#include "api_gate.cuh"
 
 }  // extern "C"

@@ -19,15 +19,14 @@ constexpr int PAIR_ATTACH_ROWS = 64;  // largest remainder that rides on a full 
 
 // Tiles of an expert with `total` rows.  Tiles never cross an expert
 // boundary.  For the CTA-pair GEMM (256-row tiles) an expert's rows past its
-// full tiles form its partial last tile; a partial tile of at most
-// PAIR_ATTACH_ROWS rows is attached to the expert's last full tile instead,
-// so the expert's weights are streamed once per feature block for both.
-__device__ __forceinline__ int expert_tile_count(int total, int tile_rows) {
+// full tiles form its partial last tile; a partial tile of at most `attach`
+// rows (PAIR_ATTACH_ROWS, or 0 for the FP8 pair GEMM) is attached to the
+// expert's last full tile instead, so the expert's weights are streamed once
+// per feature block for both.
+__device__ __forceinline__ int expert_tile_count(int total, int tile_rows, int attach) {
   int nt = (total + tile_rows - 1) / tile_rows;
-  if (tile_rows == PAIR_TILE_ROWS) {
-    const int r = total % tile_rows;
-    if (r > 0 && r <= PAIR_ATTACH_ROWS && total > tile_rows) --nt;
-  }
+  const int r = total % tile_rows;
+  if (r > 0 && r <= attach && total > tile_rows) --nt;
   return nt;
 }
 
@@ -104,7 +103,7 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* smem_warp, int* 
 // the tile table (expert, first row, rows, kind) of expert_tile, and the
 // number of tiles.
 __global__ void permute_scan(int32_t* __restrict__ chunk_counts, int n_chunks, int E,
-                             int tile_rows, int32_t* __restrict__ counts,
+                             int tile_rows, int attach, int32_t* __restrict__ counts,
                              int32_t* __restrict__ offsets, int4* __restrict__ tiles,
                              int32_t* __restrict__ num_tiles, int max_tiles,
                              unsigned int* sched_zero) {
@@ -118,7 +117,7 @@ __global__ void permute_scan(int32_t* __restrict__ chunk_counts, int n_chunks, i
     for (int c = 0; c < n_chunks; ++c) total += chunk_counts[(size_t)c * E + e];
   int all_rows;
   const int off = block_exclusive_scan(e < E ? total : 0, warp_sums, &all_rows);
-  const int nt = (e < E) ? expert_tile_count(total, tile_rows) : 0;
+  const int nt = (e < E) ? expert_tile_count(total, tile_rows, attach) : 0;
   int all_tiles;
   const int toff = block_exclusive_scan(nt, warp_sums, &all_tiles);
   if (e < E) {
@@ -298,7 +297,8 @@ __global__ void __launch_bounds__(256) permute_gather(const Tin* __restrict__ x,
 template <typename Tin>
 __device__ __forceinline__ void permute_block(
     const int32_t* idx, const float* w, const Tin* __restrict__ x, int T, int k, int E, int H,
-    int tile_rows, int max_tiles, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+    int tile_rows, int attach, int max_tiles, int32_t* __restrict__ counts,
+    int32_t* __restrict__ offsets,
     int4* __restrict__ tiles, int32_t* __restrict__ num_tiles, int32_t* __restrict__ perm_token,
     float* __restrict__ perm_w, int32_t* __restrict__ inv_row, Tin* __restrict__ x_perm,
     int* status, unsigned int* sched_zero, int* cnt, int* pos, int* warp_sums, bool gather,
@@ -323,7 +323,7 @@ __device__ __forceinline__ void permute_block(
   const int total = e < E ? cnt[e] : 0;
   int all_rows, all_tiles;
   const int off = block_exclusive_scan(total, warp_sums, &all_rows);
-  const int nt = expert_tile_count(total, tile_rows);
+  const int nt = expert_tile_count(total, tile_rows, attach);
   const int toff = block_exclusive_scan(nt, warp_sums, &all_tiles);
   if (e < E) {
     counts[e] = total;
@@ -370,6 +370,7 @@ __device__ __forceinline__ void permute_block(
 
 struct PermuteOut {
   int tile_rows, max_tiles;
+  int attach;   // remainder rows that ride on a full tile (expert_tile_count)
   int32_t *counts, *offsets;
   int4* tiles;
   int32_t *num_tiles, *perm_token;
@@ -394,8 +395,8 @@ __global__ void __launch_bounds__(512) permute_small(const int32_t* __restrict__
   __shared__ int warp_sums[33];
   pdl_wait();
   pdl_trigger();
-  permute_block(idx, w, x, T, k, E, H, o.tile_rows, o.max_tiles, o.counts, o.offsets, o.tiles,
-                o.num_tiles, o.perm_token, o.perm_w, o.inv_row, static_cast<Tin*>(o.x_perm),
+  permute_block(idx, w, x, T, k, E, H, o.tile_rows, o.attach, o.max_tiles, o.counts, o.offsets,
+                o.tiles, o.num_tiles, o.perm_token, o.perm_w, o.inv_row, static_cast<Tin*>(o.x_perm),
                 o.status, o.sched_zero, sm, sm + E, warp_sums, o.gather != 0, o.ready, o.n_ready);
 }
 

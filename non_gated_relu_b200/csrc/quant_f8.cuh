@@ -1,0 +1,188 @@
+// quant_f8.cuh -- 8-bit floating point (E4M3) operands with a scale per block
+// of 128, as the FP8 products read them.
+//
+// Activations [R, K]: one scale per row and 128 features, the least power of
+// two s with amax <= 448 s (s = 1 for a block of zeros, at least 2^-126).
+// Dividing by a power of two is exact, so the only rounding is that of x / s
+// to E4M3 (nearest even), and codes do not depend on how the quotient is
+// computed.  A value that is not finite becomes the NaN code and does not
+// count in amax.  Weights [n, rows, cols]: the same rule over 128 x 128 blocks.
+//
+// Bound by memory: 2 or 4 bytes read and 1 written per value.  Eight lanes
+// hold a block (16 values each), so its maximum is three shuffles away and each
+// lane stores 16 bytes; blocks of all rows are numbered through, which keeps
+// every lane busy at any K.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace nh {
+namespace f8 {
+
+constexpr int BLK = 128;
+
+// exponent of the block's scale from the bits of its largest magnitude (finite):
+// 448 = 1.75 * 2^8
+__device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
+  if (amax_bits == 0) return 0;
+  const int e = (int)(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, -126);
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+constexpr uint32_t INF_BITS = 0x7f800000u;
+
+// Two values times a power of two as a pair of codes (low byte first).  Scaled
+// finite values never pass 448, so only Inf and NaN give the NaN code.
+__device__ __forceinline__ uint32_t encode2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float nan_if_inf(float v) {
+  return mag_bits(v) >= INF_BITS ? __int_as_float(0x7fffffff) : v;
+}
+
+// relu(v)^2 that keeps a NaN
+__device__ __forceinline__ float relu2_nan(float v) { return v < 0.f ? 0.f : v * v; }
+
+// 16 values of a row from global memory
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 u = q[h];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
+      v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const float4 f = q[h];
+    v[4 * h] = f.x;
+    v[4 * h + 1] = f.y;
+    v[4 * h + 2] = f.z;
+    v[4 * h + 3] = f.w;
+  }
+}
+
+// bits of the largest magnitude of 16 values; Inf and NaN are left out where
+// there are any
+__device__ __forceinline__ uint32_t amax16(const float (&v)[16]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, mag_bits(v[i]));
+  if (m >= INF_BITS) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, mag_bits(v[i]) < INF_BITS ? mag_bits(v[i]) : 0u);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint4 encode16(const float (&v)[16], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = nan_if_inf(v[4 * i + j] * inv);
+    w[i] = encode2(s[0], s[1]) | (encode2(s[2], s[3]) << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows of activations.  inv_row == null: codes [R, K], scales [R, KB].  With
+// inv_row [R, k]: each row is stored to its k permuted rows instead (ids < 0:
+// no row), so the routed experts read their tokens in expert order.
+template <typename Tin>
+__global__ void __launch_bounds__(256) quantize_rows(const Tin* __restrict__ x, uint32_t units,
+                                                     int K, int KB, uint8_t* __restrict__ codes,
+                                                     float* __restrict__ scales,
+                                                     const int32_t* __restrict__ inv_row, int k) {
+  pdl_wait();
+  pdl_trigger();
+  const int sub = threadIdx.x & 7;
+  const uint32_t stride = gridDim.x * (blockDim.x >> 3);
+  const uint32_t first = blockIdx.x * (blockDim.x >> 3) + (threadIdx.x >> 3);
+  const unsigned group = 0xffu << (threadIdx.x & 24);
+  for (uint32_t u = first; u < units; u += stride) {
+    const uint32_t row = u / (uint32_t)KB, b = u - row * (uint32_t)KB;
+    const int col = (int)b * BLK + sub * 16;
+    float v[16];
+    if (col < K) {
+      load16(x + (size_t)row * K + col, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    }
+    uint32_t m = amax16(v);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(group, m, o));
+    const int e = scale_exp(m);
+    const uint4 q = encode16(v, pow2(-e));
+    if (inv_row == nullptr) {
+      if (col < K) *reinterpret_cast<uint4*>(codes + (size_t)row * K + col) = q;
+      if (sub == 0) scales[u] = pow2(e);
+    } else {
+      for (int j = 0; j < k; ++j) {
+        const int p = __ldg(inv_row + (size_t)row * k + j);
+        if (p < 0) continue;
+        if (col < K) *reinterpret_cast<uint4*>(codes + (size_t)p * K + col) = q;
+        if (sub == 0) scales[(size_t)p * KB + b] = pow2(e);
+      }
+    }
+  }
+}
+
+// One 128 x 128 block of a weight per CTA: thread = half a row (64 values).
+template <typename Tin>
+__global__ void __launch_bounds__(256) quantize_blocks(const Tin* __restrict__ w, int rows,
+                                                       int cols, int RB, int CB,
+                                                       uint8_t* __restrict__ codes,
+                                                       float* __restrict__ scales) {
+  __shared__ uint32_t part[8];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t blk = blockIdx.x;
+  const int64_t mat = blk / ((int64_t)RB * CB);
+  const int in = (int)(blk - mat * RB * CB);
+  const int r = (in / CB) * BLK + (threadIdx.x >> 1);
+  const int c0 = (in % CB) * BLK + (threadIdx.x & 1) * 64;
+  const size_t at = ((size_t)mat * rows + r) * cols;
+  float v[4][16];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (r < rows && c0 + 16 * i < cols) {
+      load16(w + at + c0 + 16 * i, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[i][j] = 0.f;
+    }
+    m = max(m, amax16(v[i]));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+  const int e = scale_exp(m);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (r < rows && c0 + 16 * i < cols)
+      *reinterpret_cast<uint4*>(codes + at + c0 + 16 * i) = encode16(v[i], pow2(-e));
+  if (threadIdx.x == 0) scales[blk] = pow2(e);
+}
+
+}  // namespace f8
+}  // namespace nh

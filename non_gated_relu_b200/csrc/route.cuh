@@ -386,6 +386,17 @@ __global__ void __launch_bounds__(256) router_fused_small(const Tin* __restrict_
   if (threadIdx.x == 0) *done = 0u;
 }
 
+// The logits alone, decode-sized T (<= 32): block e computes expert e's.
+template <typename Tin>
+__global__ void __launch_bounds__(256) router_logits_small(const Tin* __restrict__ x,
+                                                           const float* __restrict__ wr,
+                                                           float* logits, int T, int E, int H) {
+  __shared__ float red[8][32];
+  pdl_wait();
+  pdl_trigger();
+  router_block_logits(x, wr, (int)blockIdx.x, T, E, H, logits, red);
+}
+
 // fp32 router weight -> three bf16 planes [E][3H] (hi | mid | lo) with
 // w = hi + mid + lo to 24 significant bits, so that a bf16 tensor-core GEMM
 // over K = 3H reproduces the fp32-weight logits.

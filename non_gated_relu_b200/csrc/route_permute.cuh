@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(256) route_permute_small(const Tin* __restrict
   for (int t = wib; t < T; t += 8)
     select_token(a, t, logits + (size_t)t * E, sel + (size_t)wib * 2 * E, lane, s_idx, s_w);
   __syncthreads();
-  permute_block(s_idx, s_w, x, T, k, E, H, o.tile_rows, o.max_tiles, o.counts, o.offsets, o.tiles,
-                o.num_tiles, o.perm_token, o.perm_w, o.inv_row, static_cast<Tin*>(o.x_perm),
+  permute_block(s_idx, s_w, x, T, k, E, H, o.tile_rows, o.attach, o.max_tiles, o.counts, o.offsets,
+                o.tiles, o.num_tiles, o.perm_token, o.perm_w, o.inv_row, static_cast<Tin*>(o.x_perm),
                 o.status, o.sched_zero, cnt, pos, warp_sums, o.gather != 0, o.ready, o.n_ready);
   if (threadIdx.x == 0) *done = 0u;
 }

@@ -30,7 +30,7 @@ from typing import Optional, Tuple
 import numpy as np
 import torch
 
-from . import NH_WEIGHTS_NVFP4, config_from, finalize
+from . import NH_WEIGHTS_FP8, NH_WEIGHTS_NVFP4, config_from, finalize
 from .block import NemotronHMoE
 
 BLOCK = 64
@@ -146,6 +146,9 @@ class TPNemotronHMoE:
         self.cfg = cfg
         if getattr(cfg, "latent_size", 0):
             raise NotImplementedError("tensor parallelism of a latent block is not built")
+        if config_from(cfg).weight_format == NH_WEIGHTS_FP8:
+            # shards are cut in blocks of 64 features, scale blocks are 128 wide
+            raise NotImplementedError("tensor parallelism of FP8 expert weights is not built")
         self.cfg_rank = shard_config(cfg, self.world, self.rank)
         q = None
         if config_from(cfg).weight_format == NH_WEIGHTS_NVFP4:

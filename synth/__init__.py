@@ -53,7 +53,7 @@ class MoEConfig:
     norm_topk_prob: bool = True
     routed_scaling_factor: float = 2.5
     dtype: str = "bf16"          # activations and expert weights; router is fp32
-    weight_format: str = "native"  # expert / shared weights: "native" (= dtype) or "nvfp4"
+    weight_format: str = "native"  # expert / shared weights: "native" (= dtype), "nvfp4" or "fp8"
     seed: int = 0
     x_std: float = 1.0
     w_std: float = 0.02
@@ -64,6 +64,7 @@ class MoEConfig:
     tie_columns: int = 0
     latent_size: int = 0         # >0: routed experts in this width between
                                  # fc1_latent_proj [L, H] and fc2_latent_proj [H, L]
+    scoring_func: str = "sigmoid"  # router scores: "sigmoid" or "softmax"
 
     # short aliases used by the kernels' notation
     @property
