@@ -6,24 +6,29 @@
 //
 // The two scales change with every K block, so the product of a block cannot
 // stay in the tensor-memory accumulator: each block is one accumulator (four
-// MMAs of K = 32 starting from zero), two accumulators take turns, and eight
-// epilogue warps per CTA drain one into registers, times its scales, while the
-// tensor cores fill the other.  A tile is 256 rows x 256 features for a pair of
-// CTAs (each stages 128 rows of both operands), so per K block a CTA's warps
-// read 128 x 256 values and do one multiply-add each: a thread owns one row and
-// 128 features, which makes the scale one number per thread and block, keeps
-// the running sum in 128 registers, and leaves the maximum of a (row, 128)
-// block of the output inside one thread, where the next projection's
+// MMAs of K = 32 starting from zero), two accumulators take turns, and drain
+// warps read one into registers and add it up times its scales, while the tensor
+// cores fill the other.  A tile is 256 rows x 256 features for a pair of CTAs
+// (each stages 128 rows of both operands).  Per K block of a tile the MMAs take
+// 512 cycles and the multiply-adds 256 of each SM's float32 units; what sets the
+// rate is how long an accumulator is away from the tensor cores: a drain warp
+// takes its 128 columns in two loads of 64 and hands the accumulator back before
+// it adds the second.  A thread owns one row and 128 features, which makes the
+// scale one number per thread and block, and leaves the maximum of a (row, 128
+// features) block of the output inside one thread, where the next projection's
 // quantization needs it.
 //
-// Roles (384 threads): warp 0 lane 0 TMA producer (both CTAs); warp 1 tensor
-// memory owner, lane 0 of the leader issues the MMAs; warps 4..11 drain (warp
-// w: row quarter w mod 4, feature half (w - 4) / 4).  The first four warps hand
-// registers to the other eight, whose sums would spill in an even split.  Tiles are dealt out in
-// turn (tile i to pair i mod pairs): they all take the same time.  Both CTAs'
-// copies complete on the leader's stage barrier, MMA completion is committed
-// to both CTAs, the peer's drains arrive on the leader's barriers.  Every wait
-// is bounded, as in the bf16 kernels.
+// Roles (384 threads): warp 0 TMA producer (both CTAs); warp 1 tensor memory
+// owner and, in the leader, MMA issuer; warps 4..11 drain (warp w: row quarter
+// w mod 4, feature half (w - 4) / 4).  The first four warps hand registers to
+// the other eight, whose sums would spill in an even split.  Producer and
+// issuer run their loops as whole warps and elect a lane for the instruction
+// itself: descriptors and addresses then stay in uniform registers (one lane in
+// a branch of its own needed 700 cycles to issue a K block).  Tiles are dealt
+// out in turn (tile i to pair i mod pairs): they all take the same time.  Both
+// CTAs' copies complete on the leader's stage barrier, MMA completion is
+// committed to both CTAs, the peer's drains arrive on the leader's barriers.
+// Every wait is bounded, as in the bf16 kernels.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -37,13 +42,14 @@ constexpr int UMMA_K = 32;
 constexpr int MP = 256, NT = 256, HALF = 128;
 constexpr int STAGES = 6;
 constexpr int EPI_WARPS = 8;
+constexpr int COLS = 128;      // features of a drain warp's rows: one scale block
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int REGS_ROLES = 48, REGS_DRAIN = 224;   // per thread, after the split
 constexpr int REGS_NEEDED = 128 * REGS_ROLES + 32 * EPI_WARPS * REGS_DRAIN;
 constexpr int OP_BYTES = HALF * BK;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int TMEM_COLS = 2 * NT;
-constexpr int NBAR = 2 * STAGES + 5;
+constexpr int NBAR = 2 * STAGES + 3;
 constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + NBAR * 8 + 16;
 
 enum Out : int {
@@ -86,20 +92,59 @@ __device__ __forceinline__ uint32_t make_idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 32 accumulator columns of this thread's row: load and wait as one statement,
-// so that nothing that uses the values can move between the two
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 32 accumulator columns of this thread's row; the values are there after
+// tmem_wait and pin.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      :
+        "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// pin: volatile statements keep their order, so what uses the pinned registers
+// cannot move ahead of the wait before it.
+__device__ __forceinline__ void tmem_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Arrive on a barrier (a shared::cluster address) without releasing memory: what
+// it hands over is tensor memory that has been read (tcgen05.wait::ld and
+// tcgen05.fence order that), no memory contents.  A releasing arrive waits for
+// the lane's global loads in flight, 200 to 300 cycles for every accumulator.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Arrive once on the barrier at the same place in both CTAs when all prior pair
+// MMAs of this thread complete.
+__device__ __forceinline__ void umma_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
       : "memory");
 }
 
@@ -112,16 +157,27 @@ __device__ __forceinline__ int4 entry(const Args& g, int m) {
 // past N arrive as zeros and their columns are not stored)
 __device__ __forceinline__ int mma_n(int n_eff) { return (n_eff + 31) & ~31; }
 
-// One row's 128 features of the tile at its end.  n: how many of them exist
-// (a multiple of 16).
+// bits of the largest finite relu(acc)^2 among a row's first n features
+__device__ __forceinline__ uint32_t relu2_amax(int n, const float (&acc)[COLS]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) {
+    const uint32_t b = f8::mag_bits(f8::relu2_nan(acc[i]));
+    m = max(m, b < f8::INF_BITS && i < n ? b : 0u);
+  }
+  return m;
+}
+
+// One row's 128 features of the tile at its end.  n: how many of them exist (a
+// multiple of 16).
 template <int OUT>
 __device__ __forceinline__ void finish_row(const Args& g, int row, int f0, int n,
-                                           const float (&acc)[128]) {
+                                           const float (&acc)[COLS]) {
   if constexpr (OUT == OUT_BF16) {
     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) +
                                           (size_t)row * g.ldo + f0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < COLS / 8; ++i)
       if (8 * i < n)
         dst[i] = make_uint4(pack_bf16x2(acc[8 * i], acc[8 * i + 1]),
                             pack_bf16x2(acc[8 * i + 2], acc[8 * i + 3]),
@@ -130,21 +186,15 @@ __device__ __forceinline__ void finish_row(const Args& g, int row, int f0, int n
   } else if constexpr (OUT == OUT_F32) {
     float4* dst = reinterpret_cast<float4*>(static_cast<float*>(g.out) + (size_t)row * g.ldo + f0);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < COLS / 4; ++i)
       if (4 * i < n)
         dst[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
   } else if constexpr (OUT == OUT_RELU2_F8) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 128; ++i) {
-      const uint32_t b = f8::mag_bits(f8::relu2_nan(acc[i]));
-      m = max(m, b < f8::INF_BITS && i < n ? b : 0u);
-    }
-    const int e = f8::scale_exp(m);
+    const int e = f8::scale_exp(relu2_amax(n, acc));
     const float inv = f8::pow2(-e);
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.out) + (size_t)row * g.ldo + f0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < COLS / 16; ++i) {
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = f8::relu2_nan(acc[16 * i + j]);
@@ -156,7 +206,7 @@ __device__ __forceinline__ void finish_row(const Args& g, int row, int f0, int n
     const int64_t to = OUT == OUT_COMBINE ? g.dst_row[row] : row;
     float* dst = static_cast<float*>(g.out) + to * g.ldo + f0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < COLS / 4; ++i)
       if (4 * i < n)
         red_add_f32x4(dst + 4 * i, w * acc[4 * i], w * acc[4 * i + 1], w * acc[4 * i + 2],
                       w * acc[4 * i + 3]);
@@ -173,10 +223,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* const base_ptr = smem_raw + (base - raw);
   const uint32_t bar0 = base + STAGES * STAGE_BYTES;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  // a stage's MMAs are done: the producer may refill it, and the accumulator
+  // that they wrote may be drained
+  auto done_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + STAGES * STAGE_BYTES + NBAR * 8);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -186,12 +237,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+      mbar_init(done_bar(s), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // both CTAs' epilogue warps
-    }
+    for (uint32_t a = 0; a < 2; ++a) mbar_init(tempty_bar(a), 2 * EPI_WARPS);   // both CTAs' drains
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -220,130 +268,140 @@ __global__ void __launch_bounds__(THREADS, 1)
   // the split draws on what the block was launched with: the host checks that
   // the kernel's registers cover REGS_NEEDED before any launch
   if (warp < 4) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ROLES));
-   if (warp == 0 && lane == 0) {
-    // ---------------- producer ----------------
-    int stage = 0;
-    uint32_t phase = 0;
-    long issued = 0;
-    bool ok = true;
-    for (int64_t tile = pair; ok && tile < total; tile += pairs) {
-      const int m = (int)(tile / n_blocks), nb = (int)(tile - (int64_t)m * n_blocks);
-      const int4 ent = entry(g, m);
-      const int x_row = ent.y + (int)rank * HALF;
-      const int w_row = nb * NT + (int)rank * (mma_n(min(NT, g.N - nb * NT)) / 2);
-      for (int kb = 0; kb < nk; ++kb) {
-        if (!mbar_wait_spin(empty_bar(stage), phase ^ 1u, wc, SITE_TC_PRODUCER)) {
-          ok = false;
-          break;
-        }
-        const uint32_t sx = base + stage * STAGE_BYTES, sw = sx + OP_BYTES;
-        const uint32_t fb = map_to_rank(full_bar(stage), 0);
-        if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * STAGE_BYTES);
-        tma_load_2d_pair(sx, &map_x, fb, kb * BK, x_row);
-        tma_load_3d_pair(sw, &map_w, fb, kb * BK, w_row, ent.x);
-        ++issued;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ROLES));
+    if (warp == 0) {
+      // ---------------- producer ----------------
+      int stage = 0;
+      uint32_t phase = 0;
+      long issued = 0;
+      bool ok = true;
+      const uint32_t full0 = map_to_rank(full_bar(0), 0);   // the leader's stage barriers
+      for (int64_t tile = pair; ok && tile < total; tile += pairs) {
+        const int m = (int)(tile / n_blocks), nb = (int)(tile - (int64_t)m * n_blocks);
+        const int4 ent = entry(g, m);
+        const int x_row = ent.y + (int)rank * HALF;
+        const int w_row = nb * NT + (int)rank * (mma_n(min(NT, g.N - nb * NT)) / 2);
+        for (int kb = 0; kb < nk; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait_spin(done_bar(stage), phase ^ 1u, wc,
+                                                      SITE_TC_PRODUCER));
+          if (!ok) break;
+          const uint32_t sx = base + stage * STAGE_BYTES, sw = sx + OP_BYTES;
+          const uint32_t fb = full0 + 8u * stage;
+          if (elect_one()) {
+            if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * STAGE_BYTES);
+            tma_load_2d_pair(sx, &map_x, fb, kb * BK, x_row);
+            tma_load_3d_pair(sw, &map_w, fb, kb * BK, w_row, ent.x);
+          }
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
-    }
-    if (!ok && leader) {
-      // the leader's stage barriers count both CTAs' copies: wait for those in flight
-      const long first = issued > STAGES ? issued - STAGES : 0;
-      for (long i = first; i < issued; ++i)
-        tc::mbar_drain(full_bar((int)(i % STAGES)), (uint32_t)((i / STAGES) & 1), g.timeout_ns,
-                       g.status);
-    }
-  } else if (warp == 1 && lane == 0 && leader) {
-    // ---------------- MMA issuer ----------------
-    int stage = 0;
-    uint32_t phase = 0, use = 0;
-    bool ok = true, any = false;
-    for (int64_t tile = pair; ok && tile < total; tile += pairs) {
-      const int nb = (int)(tile % n_blocks);
-      const uint32_t idesc = make_idesc_e4m3(MP, mma_n(min(NT, g.N - nb * NT)));
-      for (int kb = 0; kb < nk; ++kb, ++use) {
-        const uint32_t acc = use & 1u;
-        if (!mbar_wait_cluster(tempty_bar(acc), ((use >> 1) & 1u) ^ 1u, wc, SITE_TC_MMA) ||
-            !mbar_wait_spin(full_bar(stage), phase, wc, SITE_TC_MMA)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sx = base + stage * STAGE_BYTES, sw = sx + OP_BYTES;
+      if (!ok && leader && lane == 0) {
+        // the leader's stage barriers count both CTAs' copies: wait for those in flight
+        const long first = issued > STAGES ? issued - STAGES : 0;
+        for (long i = first; i < issued; ++i)
+          tc::mbar_drain(full_bar((int)(i % STAGES)), (uint32_t)((i / STAGES) & 1), g.timeout_ns,
+                         g.status);
+      }
+    } else if (warp == 1 && leader) {
+      // ---------------- MMA issuer ----------------
+      int stage = 0;
+      uint32_t phase = 0, use = 0;
+      bool ok = true, any = false;
+      const uint64_t sdesc0 = make_sdesc_sw128(base);
+      for (int64_t tile = pair; ok && tile < total; tile += pairs) {
+        const int nb = (int)(tile % n_blocks);
+        const uint32_t idesc = make_idesc_e4m3(MP, mma_n(min(NT, g.N - nb * NT)));
+        for (int kb = 0; kb < nk; ++kb, ++use) {
+          const uint32_t acc = use & 1u;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_spin(full_bar(stage), phase, wc, SITE_TC_MMA) &&
+                              mbar_wait_spin(tempty_bar(acc), ((use >> 1) & 1u) ^ 1u, wc, SITE_TC_MMA));
+          if (!ok) break;
+          tc_fence_after();
+          // start addresses count 16-byte units in the descriptor's low bits
+          const uint64_t dx = sdesc0 + (uint64_t)(stage * (STAGE_BYTES >> 4));
+          const uint64_t dw = dx + (OP_BYTES >> 4);
+          if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < BK / UMMA_K; ++kk)
-          umma_f8_pair(tmem_base + acc * NT, make_sdesc_sw128(sx + kk * UMMA_K),
-                       make_sdesc_sw128(sw + kk * UMMA_K), idesc, kk != 0);
-        any = true;
-        umma_commit_pair(tfull_bar(acc));
-        umma_commit_pair(map_to_rank(tfull_bar(acc), 1));
-        umma_commit_pair(empty_bar(stage));
-        umma_commit_pair(map_to_rank(empty_bar(stage), 1));
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
+            for (int kk = 0; kk < BK / UMMA_K; ++kk)
+              umma_f8_pair(tmem_base + acc * NT, dx + kk * (UMMA_K >> 4), dw + kk * (UMMA_K >> 4),
+                           idesc, kk != 0);
+            umma_commit_both(done_bar(stage));
+          }
+          any = true;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
+      // the lane that issued them commits and waits for the MMAs in flight
+      if (!ok && any && elect_one()) {
+        umma_commit_pair(drain_bar);
+        tc::mbar_drain(drain_bar, 0, g.timeout_ns, g.status);
+      }
     }
-    if (!ok && any) {
-      umma_commit_pair(drain_bar);
-      tc::mbar_drain(drain_bar, 0, g.timeout_ns, g.status);
-    }
-   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_DRAIN));
     // ---------------- drain: 32 rows x 128 features per warp ----------------
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
-    uint32_t use = 0;
+    const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * COLS);
+    const uint32_t tempty0 = map_to_rank(tempty_bar(0), 0);   // the leader's
+    uint32_t use = 0, phase = 0;
+    int stage = 0;
     bool ok = true;
     for (int64_t tile = pair; ok && tile < total; tile += pairs) {
       const int m = (int)(tile / n_blocks), nb = (int)(tile - (int64_t)m * n_blocks);
       const int4 ent = entry(g, m);
-      const int f0 = nb * NT + half * 128;
-      const int n = min(128, g.N - f0);            // <= 0: no features in this half
+      const int f0 = nb * NT + half * COLS;
+      const int n = min(COLS, g.N - f0);           // <= 0: no features in this half
       const int local = (int)rank * HALF + quarter * 32 + lane;
       const int row = ent.y + min(local, ent.z - 1);
       const float* xs = g.xs + (size_t)row * nk;
       const float* ws = g.ws + ((size_t)ent.x * ((g.N + 127) / 128) + (n > 0 ? f0 / 128 : 0)) * nk;
-      float acc[128];
+      float acc[COLS];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      float s = __ldg(xs) * __ldg(ws);
+      for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
+      float sx = __ldg(xs), sw = __ldg(ws);
       for (int kb = 0; kb < nk; ++kb, ++use) {
-        const uint32_t a = use & 1u;
-        int r = 1;
-        if (lane == 0)
-          r = mbar_wait_cluster(tfull_bar(a), (use >> 1) & 1u, wc, SITE_TC_EPILOGUE) ? 1 : 0;
-        r = __shfl_sync(0xffffffffu, r, 0);
-        if (!r) {
-          ok = false;
-          break;
+        const float s = sx * sw;
+        if (kb + 1 < nk) {
+          sx = __ldg(xs + kb + 1);
+          sw = __ldg(ws + kb + 1);
+        }
+        const uint32_t a = use & 1u, from = tq + a * NT;
+        // the warp leaves together, also where a wait runs out for some lanes
+        ok = __all_sync(0xffffffffu, mbar_wait(done_bar(stage), phase, wc, SITE_TC_EPILOGUE));
+        if (!ok) break;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
         tc_fence_after();
-        const float s_next = kb + 1 < nk ? __ldg(xs + kb + 1) * __ldg(ws + kb + 1) : 0.f;
+        uint32_t v[64];
         if (n > 0) {
+          tmem_ld32(from, v);
+          tmem_ld32(from + 32, v + 32);
+          tmem_wait();
+          pin(v);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tq + a * NT + 32u * c, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              acc[32 * c + i] = fmaf(s, __uint_as_float(v[i]), acc[32 * c + i]);
-          }
+          for (int i = 0; i < 64; ++i) acc[i] = fmaf(s, __uint_as_float(v[i]), acc[i]);
+          tmem_ld32(from + 64, v);
+          tmem_ld32(from + 96, v + 32);
+          tmem_wait();
+          pin(v);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (leader)
-            mbar_arrive(tempty_bar(a));
-          else
-            mbar_arrive_cluster(map_to_rank(tempty_bar(a), 0));
+        if (lane == 0) arrive_relaxed(tempty0 + 8u * a);
+        if (n > 0) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) acc[64 + i] = fmaf(s, __uint_as_float(v[i]), acc[64 + i]);
         }
-        s = s_next;
       }
       if (ok && n > 0 && local < ent.z) finish_row<OUT>(g, row, f0, n, acc);
     }
