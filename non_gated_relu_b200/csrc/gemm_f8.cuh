@@ -50,7 +50,9 @@ constexpr int OP_BYTES = HALF * BK;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int TMEM_COLS = 2 * NT;
 constexpr int NBAR = 2 * STAGES + 3;
-constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + NBAR * 8 + 16;
+constexpr int STORE_BYTES = EPI_WARPS * 32 * 128;  // 128 bytes of each drained row
+constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + STORE_BYTES + NBAR * 8 + 16;
+static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
 
 enum Out : int {
   OUT_BF16 = 0,        // out bf16 [rows, N] = acc
@@ -148,6 +150,25 @@ __device__ __forceinline__ void umma_commit_both(uint32_t bar) {
       : "memory");
 }
 
+// acc += s v for 32 columns
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float s) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = fmaf(s, __uint_as_float(v[i]), acc[i]);
+}
+
+// A pair's tiles, `pairs` apart: (tile entry m, feature block nb)
+struct TileWalk {
+  int m, nb;
+  __device__ __forceinline__ void next(int n_blocks, int step_m, int step_nb) {
+    m += step_m;
+    nb += step_nb;
+    if (nb >= n_blocks) {
+      nb -= n_blocks;
+      ++m;
+    }
+  }
+};
+
 __device__ __forceinline__ int4 entry(const Args& g, int m) {
   if (g.tiles) return g.tiles[m];
   return make_int4(0, m * MP, min(MP, g.dense_rows - m * MP), 0);
@@ -168,48 +189,71 @@ __device__ __forceinline__ uint32_t relu2_amax(int n, const float (&acc)[COLS]) 
   return m;
 }
 
-// One row's 128 features of the tile at its end.  n: how many of them exist (a
-// multiple of 16).
+// The end of a tile: a warp's 32 rows x 128 features, a lane's row in acc.  A
+// store of 16 bytes by every lane to its own row touches 32 lines (a tile's
+// stores took 5000 to 9000 cycles that way, its K loop 15000), so the rows cross
+// shared memory 128 bytes at a time and leave four to an instruction: 16-byte
+// word j of row r waits in slot j ^ (r mod 8).  row0: first row; rows: how many
+// exist; n: features that exist (a multiple of 16).
 template <int OUT>
-__device__ __forceinline__ void finish_row(const Args& g, int row, int f0, int n,
-                                           const float (&acc)[COLS]) {
-  if constexpr (OUT == OUT_BF16) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) +
-                                          (size_t)row * g.ldo + f0);
-#pragma unroll
-    for (int i = 0; i < COLS / 8; ++i)
-      if (8 * i < n)
-        dst[i] = make_uint4(pack_bf16x2(acc[8 * i], acc[8 * i + 1]),
-                            pack_bf16x2(acc[8 * i + 2], acc[8 * i + 3]),
-                            pack_bf16x2(acc[8 * i + 4], acc[8 * i + 5]),
-                            pack_bf16x2(acc[8 * i + 6], acc[8 * i + 7]));
-  } else if constexpr (OUT == OUT_F32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(g.out) + (size_t)row * g.ldo + f0);
-#pragma unroll
-    for (int i = 0; i < COLS / 4; ++i)
-      if (4 * i < n)
-        dst[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-  } else if constexpr (OUT == OUT_RELU2_F8) {
+__device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, int f0, int n,
+                                            const float (&acc)[COLS], uint4* stage, int lane) {
+  constexpr bool F32 = OUT == OUT_F32 || OUT == OUT_ADD_F32 || OUT == OUT_COMBINE;
+  constexpr int PER = F32 ? 4 : (OUT == OUT_BF16 ? 8 : 16);   // features of a 16-byte word
+  constexpr int PASSES = COLS / (8 * PER);
+  const int mine = row0 + min(lane, rows - 1);
+  int64_t to = mine;      // output row of this lane's row
+  float w = 1.f;
+  if constexpr (OUT == OUT_COMBINE) {
+    to = g.dst_row[mine];
+    w = g.perm_w[mine];
+  }
+  if constexpr (OUT == OUT_RELU2_F8) {
     const int e = f8::scale_exp(relu2_amax(n, acc));
-    const float inv = f8::pow2(-e);
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.out) + (size_t)row * g.ldo + f0);
+    w = f8::pow2(-e);
+    if (lane < rows) g.out_scales[(size_t)mine * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
+  }
 #pragma unroll
-    for (int i = 0; i < COLS / 16; ++i) {
-      float v[16];
+  for (int p = 0; p < PASSES; ++p) {
+    __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = f8::relu2_nan(acc[16 * i + j]);
-      if (16 * i < n) dst[i] = f8::encode16(v, inv);
+    for (int j = 0; j < 8; ++j) {
+      const int c = (p * 8 + j) * PER;
+      uint4 word;
+      if constexpr (F32) {
+        word = make_uint4(__float_as_uint(w * acc[c]), __float_as_uint(w * acc[c + 1]),
+                          __float_as_uint(w * acc[c + 2]), __float_as_uint(w * acc[c + 3]));
+      } else if constexpr (OUT == OUT_BF16) {
+        word = make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
+                          pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
+      } else {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = f8::relu2_nan(acc[c + i]);
+        word = f8::encode16(v, w);
+      }
+      stage[lane * 8 + (j ^ (lane & 7))] = word;
     }
-    g.out_scales[(size_t)row * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
-  } else {
-    const float w = OUT == OUT_COMBINE ? g.perm_w[row] : 1.f;
-    const int64_t to = OUT == OUT_COMBINE ? g.dst_row[row] : row;
-    float* dst = static_cast<float*>(g.out) + to * g.ldo + f0;
+    __syncwarp();
+    const int j = lane & 7, c = (p * 8 + j) * PER;
 #pragma unroll
-    for (int i = 0; i < COLS / 4; ++i)
-      if (4 * i < n)
-        red_add_f32x4(dst + 4 * i, w * acc[4 * i], w * acc[4 * i + 1], w * acc[4 * i + 2],
-                      w * acc[4 * i + 3]);
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const uint4 word = stage[r * 8 + (j ^ (r & 7))];
+      const int64_t row = OUT == OUT_COMBINE ? __shfl_sync(0xffffffffu, (int)to, r) : row0 + r;
+      if (r < rows && c < n) {
+        const size_t at = (size_t)row * g.ldo + f0 + c;
+        if constexpr (OUT == OUT_ADD_F32 || OUT == OUT_COMBINE)
+          red_add_f32x4(static_cast<float*>(g.out) + at, __uint_as_float(word.x),
+                        __uint_as_float(word.y), __uint_as_float(word.z), __uint_as_float(word.w));
+        else if constexpr (OUT == OUT_F32)
+          *reinterpret_cast<uint4*>(static_cast<float*>(g.out) + at) = word;
+        else if constexpr (OUT == OUT_BF16)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out) + at) = word;
+        else
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.out) + at) = word;
+      }
+    }
   }
 }
 
@@ -221,14 +265,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t bar0 = base + STAGES * STAGE_BYTES;
+  const uint32_t bar0 = base + STAGES * STAGE_BYTES + STORE_BYTES;
+  uint4* const stores = reinterpret_cast<uint4*>(base_ptr + STAGES * STAGE_BYTES);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   // a stage's MMAs are done: the producer may refill it, and the accumulator
   // that they wrote may be drained
   auto done_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + a); };
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + STAGES * STAGE_BYTES + NBAR * 8);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + STAGES * STAGE_BYTES + STORE_BYTES + NBAR * 8);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t rank = cluster_rank();
@@ -261,8 +306,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int num_m = g.tiles ? *g.num_tiles : (g.dense_rows + MP - 1) / MP;
   const int n_blocks = (g.N + NT - 1) / NT;
-  const int64_t total = (int64_t)num_m * n_blocks;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int step_m = pairs / n_blocks, step_nb = pairs - step_m * n_blocks;
+  TileWalk t{pair / n_blocks, pair % n_blocks};
   const int nk = g.KB;
 
   // the split draws on what the block was launched with: the host checks that
@@ -276,9 +322,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       long issued = 0;
       bool ok = true;
       const uint32_t full0 = map_to_rank(full_bar(0), 0);   // the leader's stage barriers
-      for (int64_t tile = pair; ok && tile < total; tile += pairs) {
-        const int m = (int)(tile / n_blocks), nb = (int)(tile - (int64_t)m * n_blocks);
-        const int4 ent = entry(g, m);
+      for (; ok && t.m < num_m; t.next(n_blocks, step_m, step_nb)) {
+        const int nb = t.nb;
+        const int4 ent = entry(g, t.m);
         const int x_row = ent.y + (int)rank * HALF;
         const int w_row = nb * NT + (int)rank * (mma_n(min(NT, g.N - nb * NT)) / 2);
         for (int kb = 0; kb < nk; ++kb) {
@@ -312,8 +358,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t phase = 0, use = 0;
       bool ok = true, any = false;
       const uint64_t sdesc0 = make_sdesc_sw128(base);
-      for (int64_t tile = pair; ok && tile < total; tile += pairs) {
-        const int nb = (int)(tile % n_blocks);
+      for (; ok && t.m < num_m; t.next(n_blocks, step_m, step_nb)) {
+        const int nb = t.nb;
         const uint32_t idesc = make_idesc_e4m3(MP, mma_n(min(NT, g.N - nb * NT)));
         for (int kb = 0; kb < nk; ++kb, ++use) {
           const uint32_t acc = use & 1u;
@@ -351,28 +397,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * COLS);
     const uint32_t tempty0 = map_to_rank(tempty_bar(0), 0);   // the leader's
+    const int first = (int)rank * HALF + quarter * 32;        // the warp's rows in a tile
     uint32_t use = 0, phase = 0;
     int stage = 0;
     bool ok = true;
-    for (int64_t tile = pair; ok && tile < total; tile += pairs) {
-      const int m = (int)(tile / n_blocks), nb = (int)(tile - (int64_t)m * n_blocks);
-      const int4 ent = entry(g, m);
-      const int f0 = nb * NT + half * COLS;
+    for (; ok && t.m < num_m; t.next(n_blocks, step_m, step_nb)) {
+      const int4 ent = entry(g, t.m);
+      const int f0 = t.nb * NT + half * COLS;
       const int n = min(COLS, g.N - f0);           // <= 0: no features in this half
-      const int local = (int)rank * HALF + quarter * 32 + lane;
-      const int row = ent.y + min(local, ent.z - 1);
-      const float* xs = g.xs + (size_t)row * nk;
+      const float* xs = g.xs + (size_t)(ent.y + min(first + lane, ent.z - 1)) * nk;
       const float* ws = g.ws + ((size_t)ent.x * ((g.N + 127) / 128) + (n > 0 ? f0 / 128 : 0)) * nk;
+      float sx = __ldg(xs), sw = __ldg(ws);
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
-      float sx = __ldg(xs), sw = __ldg(ws);
       for (int kb = 0; kb < nk; ++kb, ++use) {
-        const float s = sx * sw;
-        if (kb + 1 < nk) {
-          sx = __ldg(xs + kb + 1);
-          sw = __ldg(ws + kb + 1);
-        }
         const uint32_t a = use & 1u, from = tq + a * NT;
         // the warp leaves together, also where a wait runs out for some lanes
         ok = __all_sync(0xffffffffu, mbar_wait(done_bar(stage), phase, wc, SITE_TC_EPILOGUE));
@@ -382,28 +421,39 @@ __global__ void __launch_bounds__(THREADS, 1)
           phase ^= 1u;
         }
         tc_fence_after();
-        uint32_t v[64];
+        // four loads of 32 columns, each in flight while the one before is added;
+        // the accumulator goes back before the last is added
+        uint32_t v0[32], v1[32];
+        if (n > 0) tmem_ld32(from, v0);
+        const float s = sx * sw;
+        if (kb + 1 < nk) {
+          sx = __ldg(xs + kb + 1);
+          sw = __ldg(ws + kb + 1);
+        }
         if (n > 0) {
-          tmem_ld32(from, v);
-          tmem_ld32(from + 32, v + 32);
           tmem_wait();
-          pin(v);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) acc[i] = fmaf(s, __uint_as_float(v[i]), acc[i]);
-          tmem_ld32(from + 64, v);
-          tmem_ld32(from + 96, v + 32);
+          pin(v0);
+          tmem_ld32(from + 32, v1);
+          add_scaled(acc, v0, s);
           tmem_wait();
-          pin(v);
+          pin(v1);
+          tmem_ld32(from + 64, v0);
+          add_scaled(acc + 32, v1, s);
+          tmem_wait();
+          pin(v0);
+          tmem_ld32(from + 96, v1);
+          add_scaled(acc + 64, v0, s);
+          tmem_wait();
+          pin(v1);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_relaxed(tempty0 + 8u * a);
-        if (n > 0) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) acc[64 + i] = fmaf(s, __uint_as_float(v[i]), acc[64 + i]);
-        }
+        if (n > 0) add_scaled(acc + 96, v1, s);
       }
-      if (ok && n > 0 && local < ent.z) finish_row<OUT>(g, row, f0, n, acc);
+      if (ok && n > 0 && first < ent.z)
+        finish_rows<OUT>(g, ent.y + first, min(32, ent.z - first), f0, n, acc,
+                         stores + (warp - 4) * 256, lane);
     }
   }
   tc_fence_before();
