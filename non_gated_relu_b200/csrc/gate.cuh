@@ -47,13 +47,14 @@ struct Args {
 };
 
 __device__ __forceinline__ float clean(float l) {
-  return l != l ? -INFINITY : fminf(l, 3.402823466e38f) + 0.0f;   // -0 becomes +0: they tie
+  // fmaxf drops a NaN; -0 becomes +0: they tie
+  return fminf(fmaxf(l, -INFINITY), 3.402823466e38f) + 0.0f;
 }
 
 // order-preserving key of a float that is not NaN; 0 is below every key
 __device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t u = __float_as_uint(v);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  const int u = __float_as_int(v);
+  return (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
@@ -142,10 +143,19 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* row, int E, int lane,
   }
 }
 
+template <int PER>
+__device__ __forceinline__ uint32_t max_key(const uint32_t (&key)[PER]) {
+  uint32_t m = key[0];
+#pragma unroll
+  for (int i = 1; i < PER; i += 2)
+    m = i + 1 < PER ? __vimax3_u32(m, key[i], key[i + 1]) : max(m, key[i]);
+  return m;
+}
+
 // sigmoid without overflow or cancellation at either end
 __device__ __forceinline__ float sigmoid(float l) {
   const float e = expf(-fabsf(l));
-  return l < 0.f ? e / (1.f + e) : 1.f / (1.f + e);
+  return (l < 0.f ? e : 1.f) / (1.f + e);
 }
 
 // This lane's part of the chosen experts' summed score: lanes j < k hold their
@@ -156,10 +166,10 @@ __device__ __forceinline__ float share(float l, bool softmax) {
   float u;
   if (softmax) {
     u = expf(l - top);
-  } else {
-    // e^-m sigmoid(l), m = min(0, top): l >= 0 only where m = 0
-    const float m = fminf(top, 0.f);
-    u = l < 0.f ? expf(l - m) / (1.f + expf(l)) : sigmoid(l);
+  } else if (top > -80.f) {
+    u = sigmoid(l);
+  } else {   // all underflow, or nearly: e^-top sigmoid(l), where sigmoid(l) = e^l
+    u = expf(l - top);
   }
   const float z = warp_sum(u);
   return z > 0.f ? u / z : 0.f;
@@ -303,8 +313,9 @@ __device__ __noinline__ int choose_f64(const Tin* row, const Args& a, double* c,
 }
 
 template <int PER, typename Tin>
-__global__ void __launch_bounds__(WARPS * 32) gate_forward(const Args a) {
+__global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(const Args a) {
   extern __shared__ double smem[];   // [WARPS][E]
+  __shared__ uint2 cand[WARPS][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -325,24 +336,48 @@ __global__ void __launch_bounds__(WARPS * 32) gate_forward(const Args a) {
     top = warp_max(m);
     if (top == -INFINITY) top = 0.f;
     float p = 0.f;
+    if (a.norm) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) p += expf(l[i] - top);
+      for (int i = 0; i < PER; ++i) p += __expf(l[i] - top);
+    } else {   // z is part of the weights too
+#pragma unroll
+      for (int i = 0; i < PER; ++i) p += expf(l[i] - top);
+    }
     z = warp_sum(p);
     if (z == 0.f) z = 1.f;
   }
   float c[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    c[i] = l[i];
-    if (by_score && l[i] != -INFINITY) {
-      const float s = a.softmax ? expf(l[i] - top) / z : sigmoid(l[i]);
-      c[i] = s + (a.bias ? __ldg(a.bias + e0 + i) : 0.f) + 0.0f;
+  for (int i = 0; i < PER; ++i) c[i] = l[i];
+  if (by_score) {
+    // Scores that only choose: the approximate exponential and divide, 2 + 1.2
+    // |x| and 2 units in the last place (their documented bounds), a third of the
+    // instructions.
+    if (a.softmax) {
+      const float iz = 1.f / z;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (l[i] != -INFINITY) c[i] = __expf(l[i] - top) * iz;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (l[i] != -INFINITY) c[i] = __fdividef(1.f, 1.f + __expf(-fmaxf(l[i], -80.f)));
     }
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E) c[i] += __ldg(a.bias + e0 + i);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] += 0.0f;
   }
-  // Twice the float32 error of a score.  sigmoid: expf and a divide, under 4
-  // roundings of a value <= 1.  softmax: those, and up to PER + 5 adds of z, of
-  // a value <= 1 / z.  The add of the bias is counted at the comparison.
-  const float tol_s = a.softmax ? (PER + 10) * 0x1p-22f / z : 0x1p-20f;
+  // Twice the error of a score, in u = 2^-24.  sigmoid, e = exp(-l): s (1 - s) <=
+  // 1/4 of e's 4 + 2.4 |l| (s (1 - s) |l| <= 0.23: under 1.6 together), the add 1,
+  // the divide 4: under 7.  softmax, of a value <= 1 / z: e^-d (4 + 2.4 d) <= 4,
+  // the rounding of l - top under 1, z's terms under 12 (512 of them at the d that
+  // counts most) and its PER + 5 adds, two roundings: under PER + 24.  The add of
+  // the bias is counted at the comparison.
+  const float tol_s = a.softmax ? (PER + 14) * 0x1p-22f / z : 0x1p-20f;
   bool again = false;
 
   uint32_t key[PER];
@@ -398,28 +433,66 @@ __global__ void __launch_bounds__(WARPS * 32) gate_forward(const Args a) {
   int my_e = 0;
   uint32_t my_key = 0u, next_key = 0u;
   const int rounds = by_score ? k + 1 : k;
-  for (int j = 0; j < rounds; ++j) {
-    uint32_t bk = key[0];
-    int bi = 0;
+  uint32_t best = max_key<PER>(key);
+  // Every one of the `rounds` best is at least the rounds-th largest of the lanes'
+  // best keys.  The few keys that are (11 of 256 at 9 rounds) go to shared memory,
+  // one to a lane, and each counts those before it: 150 instructions where one
+  // maximum after the other takes 50 a round.
+  uint32_t floor_key = 0u, left = best;
+  for (int j = 0; j < rounds; ++j) {     // lanes with equal keys fall together: a lower floor
+    floor_key = __reduce_max_sync(FULL, left);
+    if (left == floor_key) left = 0u;
+  }
+  floor_key = max(floor_key, 1u);
+  int found = 0;
 #pragma unroll
-    for (int i = 1; i < PER; ++i)
-      if (key[i] > bk) {
-        bk = key[i];
-        bi = i;
+  for (int i = 0; i < PER; ++i) {
+    const unsigned who = __ballot_sync(FULL, key[i] >= floor_key);
+    if (key[i] >= floor_key) {
+      const int at = found + __popc(who & ((1u << lane) - 1u));
+      if (at < 32) cand[warp][at] = make_uint2(key[i], (uint32_t)(e0 + i));
+    }
+    found += __popc(who);
+  }
+  if (found <= 32 && rounds <= 32) {
+    __syncwarp();
+    const uint2 me = lane < found ? cand[warp][lane] : make_uint2(0u, 0u);
+    int rank = 0;
+    for (int j = 0; j < found; ++j) {
+      const uint2 o = cand[warp][j];
+      rank += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < found && rank < rounds) cand[warp][rank] = me;
+    __syncwarp();
+    if (lane < min(found, rounds)) {
+      my_key = cand[warp][lane].x;
+      my_e = (int)cand[warp][lane].y;
+    }
+  } else {
+    // many equal keys, few lanes with many kept experts, or k = 32
+    for (int j = 0; j < rounds; ++j) {
+      const uint32_t m = __reduce_max_sync(FULL, best);
+      const int src = __ffs(__ballot_sync(FULL, best == m)) - 1;
+      int e = 0;
+      if (lane == src) {
+        // the first of this lane's keys that is the maximum goes out of the race
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (key[i] == m) {
+            key[i] = 0u;
+            e = e0 + i;
+            break;
+          }
+        best = max_key<PER>(key);
       }
-    const uint32_t m = __reduce_max_sync(FULL, bk);
-    const int src = __ffs(__ballot_sync(FULL, bk == m)) - 1;
-    const int e = __shfl_sync(FULL, e0 + bi, src);
-    if (lane == src) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i == bi) key[i] = 0u;
+      e = __shfl_sync(FULL, e, src);
+      if (lane == j) {
+        my_e = e;
+        my_key = m;
+      }
+      if (j == 32) next_key = m;   // the runner-up at k = 32, which no lane holds
     }
-    if (lane == j) {
-      my_e = e;
-      my_key = m;
-    }
-    if (j == k) next_key = m;   // the runner-up: in lane k too, if there is one
   }
   const auto logit_of = [&](int e) { return clean(to_f32(row[e])); };
   if (by_score) {
