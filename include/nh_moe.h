@@ -170,10 +170,10 @@ typedef struct {
     int32_t swap_ab;      /* 1: weights on the MMA M side (small T, or NVFP4)   */
     int32_t x_direct;     /* 1: the up projection reads x itself (no x_perm)    */
     /* With NH_WEIGHTS_FP8, written by the up projection's call: x_perm holds the
-     * E4M3 codes of x ([T, H] with x_direct, else [rows, H] in permuted order) and
-     * behind them, 256-byte aligned, their scales float [.., ceil(H / 128)]; h
-     * holds the codes of relu^2(up) [rows, I], their scales and, with x_direct,
-     * relu^2(up) itself in float32.  swap_ab and x_direct are 1 up to 32 tokens. */
+     * E4M3 codes of x [rows, H] in permuted order and behind them, 256-byte
+     * aligned, their scales float [rows, ceil(H / 128)]; h holds the codes of
+     * relu^2(up) [rows, I] and their scales.  x_direct is 0; swap_ab is 1 while
+     * an expert has few rows in the mean (tile entries of up to 128 rows). */
 } nh_moe_ws_layout;
 
 /* Validate a configuration (no device work). */
@@ -502,7 +502,7 @@ nh_status nh_fp8_quantize_weight(int64_t n_mat, int64_t rows, int64_t cols, cons
  *   aligned, holding a status word (cleared by the caller, once:
  *   nh_moe_reset_status; this call records device faults in it) and the
  *   quantized x.  Calls that may overlap need their own ws.
- * Up to 32 tokens run as a GEMV over the weights, more on tensor-core tiles; for
+ * Up to 32 tokens run as a GEMV over the weights, more on 256 x 256 tiles; for
  * given inputs a result does not depend on scheduling.
  */
 nh_status nh_fp8_linear_workspace_size(int64_t T, int64_t N, int64_t K, size_t *bytes);

@@ -91,8 +91,6 @@ nh_status nh_fp8_linear(int64_t T, int64_t N, int64_t K, const void* x, int32_t 
   c.rows = T;
   c.N = (int)N;
   c.K = (int)K;
-  c.gemv = T <= F8_GEMV_ROWS;
-  c.tile_rows = T <= 8 ? 8 : (T <= 16 ? 16 : F8_GEMV_ROWS);
   c.out_kind = y_dtype == NH_BF16 ? F8_BF16 : F8_F32;
   c.out = y;
   c.status = static_cast<int*>(ws);
@@ -105,16 +103,14 @@ nh_status nh_fp8_linear(int64_t T, int64_t N, int64_t K, const void* x, int32_t 
 static nh_status f8_experts_up(const Plan& p, int64_t T, const void* x, const nh_fp8_weight* w,
                                void* ws, int dev, cudaStream_t st) {
   const nh_moe_ws_layout& L = p.lay;
-  const bool gemv = L.swap_ab != 0;
-  const int64_t x_rows = gemv ? T : p.rows;
   uint8_t* xq = at<uint8_t>(ws, L.x_perm);
-  float* xs = at<float>(ws, L.x_perm + f8_scales_at(x_rows, p.H));
+  float* xs = at<float>(ws, L.x_perm + f8_scales_at(p.rows, p.H));
   NH_TRY(launch_quantize(static_cast<const __nv_bfloat16*>(x), T, p.H, xq, xs,
-                         gemv ? nullptr : at<int32_t>(ws, L.inv_row), p.k, dev, st));
+                         at<int32_t>(ws, L.inv_row), p.k, dev, st));
   F8Call c{};
   c.x = xq;
   c.xs = xs;
-  c.x_rows = x_rows;
+  c.x_rows = p.rows;
   c.w = w;
   c.n_exp = p.E;
   c.rows = p.rows;
@@ -124,8 +120,6 @@ static nh_status f8_experts_up(const Plan& p, int64_t T, const void* x, const nh
   c.num_tiles = at<int32_t>(ws, L.num_tiles);
   c.max_tiles = L.max_tiles;
   c.tile_rows = L.tile_rows;
-  c.gemv = gemv;
-  c.row_token = at<int32_t>(ws, L.perm_token);
   c.status = at<int>(ws, L.status);
   c.early_w = true;   // the launch before is this call's quantization
   return run_f8_up(c, f8_hidden(at<void>(ws, L.h), p.rows, p.I), dev, st);
@@ -148,7 +142,6 @@ static nh_status f8_experts_down(const Plan& p, const nh_fp8_weight* w, void* ws
   c.num_tiles = at<int32_t>(ws, L.num_tiles);
   c.max_tiles = L.max_tiles;
   c.tile_rows = L.tile_rows;
-  c.gemv = L.swap_ab != 0;
   c.out_kind = F8_COMBINE;
   c.out = y_acc;
   c.perm_w = at<float>(ws, L.perm_w);
@@ -234,8 +227,6 @@ static nh_status f8_shared(const nh_moe_config* cfg, int64_t T, const void* x,
   c.rows = T;
   c.N = p.S;
   c.K = p.H;
-  c.tile_rows = p.lay.tile_rows;
-  c.gemv = p.lay.swap_ab != 0;
   c.status = status;
   c.early_w = true;   // the launch before is this call's quantization
   NH_TRY(run_f8_up(c, h, dev, st));

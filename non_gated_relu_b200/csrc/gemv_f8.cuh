@@ -1,10 +1,9 @@
-// gemv_f8.cuh -- block-scaled FP8 product for few rows (at most 32 per
-// expert): the decode form of the FP8 experts, shared expert and linear layer.
+// gemv_f8.cuh -- block-scaled FP8 product of at most 32 dense rows: the decode
+// form of the FP8 shared expert and linear layer.
 //
 //   out[r, n] = epi( sum_b sx[r, b] sw[n / 128, b] (xq[r] . wq[n] over block b) )
 //
-// Bound by the weights' bytes.  A CTA takes 16 weight rows of one tile entry
-// over the whole K and its 8 warps take K blocks of 128 in turn, so the bytes
+// Bound by the weights' bytes.  A CTA takes 16 weight rows over the whole K and its 8 warps take K blocks of 128 in turn, so the bytes
 // of a task are all asked for at once: lane (g, q) loads 16 bytes of rows g and
 // g + 8 at 16 q of each half block, straight into the fragments of
 // mma.sync m16n8k32 (E4M3, float32 accumulate).  The order of features inside
@@ -28,26 +27,19 @@ enum Out : int {
   OUT_F32 = 1,        // out f32 [rows, N] = acc
   OUT_RELU2_F32 = 2,  // out f32 [rows, N] = relu(acc)^2   (quantized by the next kernel)
   OUT_ADD_F32 = 3,    // out f32 [rows, N] += acc, atomic adds
-  OUT_COMBINE = 4,    // out f32: out[dst_row[r]] += perm_w[r] * acc, atomic adds
 };
 
 struct Args {
-  const uint8_t* x;        // codes [rows of x, K]
-  const float* xs;         // scales [rows of x, KB]
-  const uint8_t* w;        // codes [E, N, K]
-  const float* ws;         // scales [E, ceil(N / 128), KB]
-  const int4* tiles;       // (expert, first row, rows, -) or null: dense rows
-  const int32_t* num_tiles;
-  int dense_rows, tile_rows;
+  const uint8_t* x;        // codes [rows, K]
+  const float* xs;         // scales [rows, KB]
+  const uint8_t* w;        // codes [N, K]
+  const float* ws;         // scales [ceil(N / 128), KB]
+  int rows;                // at most NT
   int N, K, KB;
-  const int32_t* row_token;  // row r reads x row row_token[r]; null: row r
   int out_kind;
-  void* out;
-  int64_t ldo;
-  const float* perm_w;
-  const int32_t* dst_row;
-  int early_w;             // weights and tile table were complete before the
-                           // previous launch in the stream began its work
+  void* out;               // [rows, N]
+  int early_w;             // weights were complete before the previous launch in
+                           // the stream began its work
 };
 
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -66,16 +58,14 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
   return v;
 }
 
-// NT: rows of a tile entry, padded (8, 16, 32); U: K blocks of a warp in flight
+// NT: rows, padded (8, 16, 32); U: K blocks of a warp in flight
 template <int NT, int U>
 __global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
   constexpr int NB = NT / 8;
   __shared__ float red[WARPS][MT][NT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
-  const int n_rb = a.N / MT;
-  const int m = blockIdx.x / n_rb, rb = blockIdx.x - m * n_rb;
-  const int n0 = rb * MT;
+  const int n0 = blockIdx.x * MT;
   const uint4 zero = make_uint4(0, 0, 0, 0);
 
   bool waited = false;
@@ -85,19 +75,9 @@ __global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
     waited = true;
   };
   if (!a.early_w) wait_previous();
-  int4 ent = make_int4(0, m * a.tile_rows, 0, 0);
-  if (a.tiles != nullptr) {
-    if (m >= *a.num_tiles) {
-      if (!waited) wait_previous();
-      return;
-    }
-    ent = a.tiles[m];
-  } else {
-    ent.z = min(a.tile_rows, a.dense_rows - ent.y);
-  }
-  const uint8_t* w0 = a.w + ((size_t)ent.x * a.N + n0 + gq) * a.K;
+  const uint8_t* w0 = a.w + ((size_t)n0 + gq) * a.K;
   const uint8_t* w1 = w0 + (size_t)8 * a.K;
-  const float* ws = a.ws + ((size_t)ent.x * ((a.N + 127) / 128) + n0 / 128) * a.KB;
+  const float* ws = a.ws + (size_t)(n0 / 128) * a.KB;
 
   float acc[NB][4];
 #pragma unroll
@@ -106,11 +86,16 @@ __global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
 
   // x rows of this lane's fragment columns (token gq of each n-tile) and of its
-  // accumulator columns (tokens 2 tq, 2 tq + 1); rows past the entry repeat its
-  // last row and are not stored
+  // accumulator columns (tokens 2 tq, 2 tq + 1); rows past the last repeat it and
+  // are not stored
   const uint8_t* xp[NB];
   const float* sp[NB][2];
-  bool have_rows = false;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    xp[j] = a.x + (size_t)min(8 * j + gq, a.rows - 1) * a.K;
+    sp[j][0] = a.xs + (size_t)min(8 * j + 2 * tq, a.rows - 1) * a.KB;
+    sp[j][1] = a.xs + (size_t)min(8 * j + 2 * tq + 1, a.rows - 1) * a.KB;
+  }
 
   for (int b0 = warp; b0 < a.KB; b0 += WARPS * U) {
     uint4 wv[U][4];
@@ -128,25 +113,13 @@ __global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
       sw[u] = b < a.KB ? __ldg(ws + b) : 0.f;
     }
     if (!waited) wait_previous();
-    if (!have_rows) {
-      have_rows = true;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int r = ent.y + min(8 * j + gq, ent.z - 1);
-        const int r0 = ent.y + min(8 * j + 2 * tq, ent.z - 1);
-        const int r1 = ent.y + min(8 * j + 2 * tq + 1, ent.z - 1);
-        xp[j] = a.x + (size_t)(a.row_token ? a.row_token[r] : r) * a.K;
-        sp[j][0] = a.xs + (size_t)(a.row_token ? a.row_token[r0] : r0) * a.KB;
-        sp[j][1] = a.xs + (size_t)(a.row_token ? a.row_token[r1] : r1) * a.KB;
-      }
-    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int b = b0 + u * WARPS;
       if (b >= a.KB) break;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        if (8 * j >= ent.z) break;
+        if (8 * j >= a.rows) break;
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -175,20 +148,16 @@ __global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
   __syncthreads();
   for (int i = threadIdx.x; i < MT * NT; i += WARPS * 32) {
     const int f = i % MT, c = i / MT;
-    if (c >= ent.z) break;
+    if (c >= a.rows) break;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) v += red[w][f][c];
-    const int r = ent.y + c;
-    const size_t at = (size_t)r * a.ldo + n0 + f;
+    const size_t at = (size_t)c * a.N + n0 + f;
     switch (a.out_kind) {
       case OUT_BF16: static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v); break;
       case OUT_F32: static_cast<float*>(a.out)[at] = v; break;
       case OUT_RELU2_F32: static_cast<float*>(a.out)[at] = f8::relu2_nan(v); break;
-      case OUT_ADD_F32: red_add_f32(static_cast<float*>(a.out) + at, v); break;
-      default:
-        red_add_f32(static_cast<float*>(a.out) + (size_t)a.dst_row[r] * a.ldo + n0 + f,
-                    a.perm_w[r] * v);
+      default: red_add_f32(static_cast<float*>(a.out) + at, v);
     }
   }
 }

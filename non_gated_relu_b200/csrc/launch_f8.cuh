@@ -1,13 +1,14 @@
 // launch_f8.cuh -- host side of the FP8 operators: tensor maps, kernel choice
 // and launches.  Part of nh_moe.cu (inside namespace nh).
 
-// uint8 [rows, row_bytes], box 128 bytes x 128 rows, 128-byte swizzle
-static nh_status map_u8_2d(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows) {
+// uint8 [rows, row_bytes], box 128 bytes x box_rows, 128-byte swizzle
+static nh_status map_u8_2d(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows,
+                           int box_rows) {
   auto fn = encode_fn();
   if (!fn) return fail(NH_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  cuuint32_t box[2] = {(cuuint32_t)f8g::BK, (cuuint32_t)f8g::HALF};
+  cuuint32_t box[2] = {(cuuint32_t)f8g::BK, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
                   es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -35,12 +36,10 @@ struct F8Call {
   const int4* tiles;
   const int32_t* num_tiles;
   int max_tiles;
-  int tile_rows;
-  bool gemv;
+  int tile_rows;             // of tile entries: below 256 with the weights on the M side
   F8Out out_kind;
-  void* out;                 // F8_RELU2: codes (pair GEMM) or float32 (GEMV)
-  float* out_scales;         // F8_RELU2 of the pair GEMM
-  const int32_t* row_token;
+  void* out;                 // F8_RELU2: codes, or float32 from the GEMV
+  float* out_scales;         // F8_RELU2: their scales (not the GEMV)
   const float* perm_w;
   const int32_t* dst_row;
   int* status;
@@ -53,38 +52,63 @@ static nh_status launch_f8_gemv(const F8Call& c, cudaStream_t st) {
   a.xs = c.xs;
   a.w = c.w->codes;
   a.ws = c.w->scales;
-  a.tiles = c.tiles;
-  a.num_tiles = c.num_tiles;
-  a.dense_rows = (int)c.rows;
-  a.tile_rows = c.tile_rows;
+  a.rows = (int)c.rows;
   a.N = c.N;
   a.K = c.K;
   a.KB = (int)f8_blocks(c.K);
-  a.row_token = c.row_token;
   switch (c.out_kind) {
     case F8_BF16: a.out_kind = f8v::OUT_BF16; break;
     case F8_F32: a.out_kind = f8v::OUT_F32; break;
     case F8_RELU2: a.out_kind = f8v::OUT_RELU2_F32; break;
     case F8_ADD: a.out_kind = f8v::OUT_ADD_F32; break;
-    default: a.out_kind = f8v::OUT_COMBINE;
+    default: return fail(NH_ERR_UNSUPPORTED, "internal: the FP8 GEMV has no combine");
   }
   a.out = c.out;
-  a.ldo = c.N;
+  a.early_w = c.early_w ? 1 : 0;
+  const dim3 g((unsigned)(c.N / f8v::MT)), b(f8v::WARPS * 32);
+  if (c.rows <= 8) return launch_k("f8_gemv", f8v::f8_gemv<8, 3>, g, b, 0, st, a);
+  if (c.rows <= 16) return launch_k("f8_gemv", f8v::f8_gemv<16, 2>, g, b, 0, st, a);
+  return launch_k("f8_gemv", f8v::f8_gemv<32, 2>, g, b, 0, st, a);
+}
+
+// the routed experts' products with weights on the MMA M side
+template <int NT, int STAGES, int CTAS>
+static nh_status launch_f8_swap_as(const F8Call& c, int dev, cudaStream_t st) {
+  using S = f8s::Shape<NT, STAGES, CTAS>;
+  CUtensorMap mx, mw;
+  NH_TRY(map_u8_2d(&mx, c.x, c.K, c.x_rows, NT));
+  NH_TRY(map_u8_3d(&mw, c.w->codes, c.K, c.N, c.n_exp, f8s::BK, true));
+  f8s::Args a{};
+  a.xs = c.xs;
+  a.ws = c.w->scales;
+  a.tiles = c.tiles;
+  a.num_tiles = c.num_tiles;
+  a.N = c.N;
+  a.K = c.K;
+  a.KB = (int)f8_blocks(c.K);
+  a.out = c.out;
+  a.out_scales = c.out_scales;
   a.perm_w = c.perm_w;
   a.dst_row = c.dst_row;
+  a.status = c.status;
+  a.timeout_ns = timeout_ns();
   a.early_w = c.early_w ? 1 : 0;
   // an entry holds at least one row
-  const int64_t m = c.tiles ? std::min<int64_t>(c.max_tiles, c.rows)
-                            : (c.rows + c.tile_rows - 1) / c.tile_rows;
-  const int64_t grid = m * (c.N / f8v::MT);
-  if (grid <= 0) return NH_OK;
-  if (grid > 0x7fffffff) return fail(NH_ERR_UNSUPPORTED, "FP8 GEMV: %lld tasks", (long long)grid);
-  const dim3 g((unsigned)grid), b(f8v::WARPS * 32);
+  const int64_t tiles = std::min<int64_t>(c.max_tiles, c.rows) * ((c.N + f8s::M - 1) / f8s::M);
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, (int64_t)g_sm_count[dev] * CTAS));
+  if (c.out_kind == F8_RELU2)
+    return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_RELU2_F8>, grid,
+                    dim3(f8s::THREADS), S::SMEM, st, mx, mw, a);
+  return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_COMBINE>, grid,
+                  dim3(f8s::THREADS), S::SMEM, st, mx, mw, a);
+}
+
+static nh_status launch_f8_swap(const F8Call& c, int dev, cudaStream_t st) {
   switch (c.tile_rows) {
-    case 8: return launch_k("f8_gemv", f8v::f8_gemv<8, 3>, g, b, 0, st, a);
-    case 16: return launch_k("f8_gemv", f8v::f8_gemv<16, 2>, g, b, 0, st, a);
-    case 32: return launch_k("f8_gemv", f8v::f8_gemv<32, 2>, g, b, 0, st, a);
-    default: return fail(NH_ERR_UNSUPPORTED, "FP8 GEMV rows %d", c.tile_rows);
+    case 16: return launch_f8_swap_as<16, 5, 2>(c, dev, st);
+    case 32: return launch_f8_swap_as<32, 5, 2>(c, dev, st);
+    case 64: return launch_f8_swap_as<64, 4, 2>(c, dev, st);
+    default: return launch_f8_swap_as<128, 6, 1>(c, dev, st);
   }
 }
 
@@ -92,7 +116,7 @@ template <int OUT>
 static nh_status launch_f8_pair_as(const F8Call& c, const f8g::Args& a, int64_t tiles, int dev,
                                    cudaStream_t st) {
   CUtensorMap mx, mw;
-  NH_TRY(map_u8_2d(&mx, c.x, c.K, c.x_rows));
+  NH_TRY(map_u8_2d(&mx, c.x, c.K, c.x_rows, f8g::HALF));
   NH_TRY(map_u8_3d(&mw, c.w->codes, c.K, c.N, c.n_exp, f8g::BK, true));
   const int64_t pairs = std::min<int64_t>(tiles, g_f8_clusters[dev]);
   if (pairs <= 0) return NH_OK;
@@ -144,9 +168,13 @@ static nh_status launch_f8_pair(const F8Call& c, int dev, cudaStream_t st) {
   }
 }
 
+static bool f8_gemv_rows(const F8Call& c) { return !c.tiles && c.rows <= F8_GEMV_ROWS; }
+
 static nh_status run_f8(const F8Call& c, int dev, cudaStream_t st) {
   if (c.rows == 0) return NH_OK;
-  return c.gemv ? launch_f8_gemv(c, st) : launch_f8_pair(c, dev, st);
+  if (c.tiles && c.tile_rows < f8g::MP) return launch_f8_swap(c, dev, st);
+  if (f8_gemv_rows(c)) return launch_f8_gemv(c, st);
+  return launch_f8_pair(c, dev, st);
 }
 
 // Quantize R rows of C values; with inv_row each to its k permuted rows.
@@ -177,9 +205,10 @@ static F8Hidden f8_hidden(void* base, int64_t R, int64_t C) {
 // set here from `h`
 static nh_status run_f8_up(F8Call c, const F8Hidden& h, int dev, cudaStream_t st) {
   c.out_kind = F8_RELU2;
-  c.out = c.gemv ? static_cast<void*>(h.f32) : h.codes;
+  const bool gemv = f8_gemv_rows(c);
+  c.out = gemv ? static_cast<void*>(h.f32) : h.codes;
   c.out_scales = h.scales;
   NH_TRY(run_f8(c, dev, st));
-  if (!c.gemv) return NH_OK;
+  if (!gemv) return NH_OK;
   return launch_quantize(h.f32, c.rows, c.N, h.codes, h.scales, nullptr, 0, dev, st);
 }

@@ -19,6 +19,7 @@
 #include "gemv_q4.cuh"
 #include "gemv_bf16.cuh"
 #include "gemm_f8.cuh"
+#include "gemm_f8s.cuh"
 #include "gemv_f8.cuh"
 #include "gate.cuh"
 #include "permute.cuh"
@@ -81,7 +82,7 @@ constexpr int ROUTE_PERMUTE_MAX_E = 256;
 // fused decode router + permute: 8 warps x 2E selection floats + E + 3 T k
 constexpr int ROUTE_PERMUTE_SMEM_MAX = (16 * 256 + 256 + 3 * 32 * 32) * 4;
 
-constexpr int F8_GEMV_ROWS = 32;   // rows up to which the FP8 products run as GEMVs
+constexpr int F8_GEMV_ROWS = 32;   // rows up to which dense FP8 products run as GEMVs
 
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -93,8 +94,8 @@ static size_t f8_scales_at(int64_t R, int64_t C) { return align_up((size_t)R * C
 static size_t f8_rows_bytes(int64_t R, int64_t C) {
   return f8_scales_at(R, C) + align_up((size_t)R * f8_blocks(C) * 4, ALIGN);
 }
-// The experts' hidden rows: quantized, and behind them in float32 where a GEMV
-// wrote them before their quantization
+// The shared expert's hidden rows: quantized, and behind them in float32 where a
+// GEMV wrote them before their quantization
 static size_t f8_hidden_bytes(int64_t R, int64_t C, bool gemv) {
   return f8_rows_bytes(R, C) + (gemv ? (size_t)R * C * 4 : 0);
 }
@@ -165,9 +166,10 @@ static void tile_plan(const nh_moe_config* c, int64_t T, int* tile_rows, int* sw
     *tile_rows = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
     *swap = 1;
   } else if (c->weight_format == NH_WEIGHTS_FP8) {
-    // up to F8_GEMV_ROWS tokens: weight rows on the MMA M side, 8 tokens on N
-    *tile_rows = T <= 8 ? 8 : (T <= 16 ? 16 : (T <= F8_GEMV_ROWS ? F8_GEMV_ROWS : f8g::MP));
-    *swap = T <= F8_GEMV_ROWS ? 1 : 0;
+    // weights on the MMA M side while an expert has few rows (mean of T k / E)
+    const int64_t mean = T * c->num_experts_per_tok / c->n_routed_experts;
+    *tile_rows = mean <= 6 ? 16 : (mean <= 16 ? 32 : (mean <= 40 ? 64 : (mean <= 100 ? 128 : f8g::MP)));
+    *swap = *tile_rows < f8g::MP ? 1 : 0;
   } else if (c->dtype == NH_F32) {
     *tile_rows = SG_BM;
     *swap = 0;
@@ -230,9 +232,9 @@ static nh_status make_plan(const nh_moe_config* c, int64_t T, Plan* p) {
   L.tiles = take((size_t)L.max_tiles * 16);
   L.num_tiles = take(4);
   if (c->weight_format == NH_WEIGHTS_FP8) {
-    L.x_direct = sw;   // GEMV: the up projection reads the tokens' rows of x (quantized)
-    L.x_perm = take(f8_rows_bytes(sw ? T : rows, p->H));
-    L.h = take(f8_hidden_bytes(rows, p->I, sw != 0));
+    L.x_direct = 0;
+    L.x_perm = take(f8_rows_bytes(rows, p->H));
+    L.h = take(f8_rows_bytes(rows, p->I));
   } else {
     L.x_perm = take(L.x_direct ? 0 : (size_t)rows * p->H * p->elem);
     L.h = take((size_t)rows * p->I * p->elem);
@@ -335,6 +337,16 @@ static nh_status f8_pair_attrs(Kern kernel) {
   return NH_OK;
 }
 
+template <int NT, int STAGES, int CTAS>
+static nh_status f8_swap_attrs() {
+  constexpr int smem = f8s::Shape<NT, STAGES, CTAS>::SMEM;
+  NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_RELU2_F8>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_COMBINE>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  return NH_OK;
+}
+
 static nh_status set_attrs(int dev) {
   cudaDeviceProp prop;
   NH_CUDA(cudaGetDeviceProperties(&prop, dev));
@@ -369,6 +381,10 @@ static nh_status set_attrs(int dev) {
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_RELU2_F8>));
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_ADD_F32>));
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_COMBINE>));
+  NH_TRY((f8_swap_attrs<16, 5, 2>()));
+  NH_TRY((f8_swap_attrs<32, 5, 2>()));
+  NH_TRY((f8_swap_attrs<64, 4, 2>()));
+  NH_TRY((f8_swap_attrs<128, 6, 1>()));
   {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(2 * (prop.multiProcessorCount / 2), 1, 1);
@@ -990,7 +1006,7 @@ nh_status nh_moe_shared_workspace_size(const nh_moe_config* cfg, int64_t T, size
   NH_TRY(make_plan(cfg, T, &p));
   if (!cfg->n_shared_experts) return fail(NH_ERR_INVALID_ARG, "config has no shared expert");
   if (cfg->weight_format == NH_WEIGHTS_FP8)
-    *bytes = ALIGN + f8_rows_bytes(T, p.H) + f8_hidden_bytes(T, p.S, p.lay.swap_ab != 0);
+    *bytes = ALIGN + f8_rows_bytes(T, p.H) + f8_hidden_bytes(T, p.S, T <= F8_GEMV_ROWS);
   else
     *bytes = ALIGN + align_up((size_t)T * p.S * p.elem + 1, ALIGN);
   return NH_OK;

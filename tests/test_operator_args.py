@@ -185,16 +185,16 @@ def test_fp8_weight_format_and_its_entry_points():
     assert rc == nh.NH_ERR_INVALID_ARG and b"latent_size" in lib.nh_last_error()
 
 
-@pytest.mark.parametrize("T", [0, 1, 8, 9, 32, 33, 300])
+@pytest.mark.parametrize("T", [0, 1, 8, 9, 32, 33, 300, 5000])
 def test_fp8_workspace_holds_codes_and_scales(T):
     cfg = synth.CONFIGS["decode_bf16_t8"].replace(weight_format="fp8")
     L = nh.workspace_layout(cfg, T)
-    rows, gemv = T * cfg.k, T <= 32
-    assert (L.swap_ab, L.x_direct) == (int(gemv), int(gemv))
-    assert L.tile_rows >= T if gemv else L.tile_rows == 256
-    x_rows = T if gemv else rows
-    assert L.h - L.x_perm >= x_rows * (cfg.H + 4 * -(-cfg.H // 128))
-    assert L.ready - L.h >= rows * (cfg.I + 4 * -(-cfg.I // 128) + (4 * cfg.I if gemv else 0))
+    rows = T * cfg.k
+    assert L.x_direct == 0 and L.swap_ab == int(L.tile_rows < 256)
+    assert L.tile_rows in (16, 32, 64, 128, 256)
+    assert L.max_tiles >= -(-rows // L.tile_rows) + min(rows, cfg.E - 1)
+    assert L.h - L.x_perm >= rows * (cfg.H + 4 * -(-cfg.H // 128))
+    assert L.ready - L.h >= rows * (cfg.I + 4 * -(-cfg.I // 128))
     assert L.total_bytes == nh.workspace_size(cfg, T)
 
 
