@@ -173,7 +173,7 @@ typedef struct {
      * E4M3 codes of x [rows, H] in permuted order and behind them, 256-byte
      * aligned, their scales float [rows, ceil(H / 128)]; h holds the codes of
      * relu^2(up) [rows, I] and their scales.  x_direct is 0; swap_ab is 1 while
-     * an expert has few rows in the mean (tile entries of up to 128 rows). */
+     * an expert has few rows in the mean (tile entries of up to 64 rows). */
 } nh_moe_ws_layout;
 
 /* Validate a configuration (no device work). */

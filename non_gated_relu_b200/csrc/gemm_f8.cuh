@@ -178,13 +178,30 @@ __device__ __forceinline__ int4 entry(const Args& g, int m) {
 // past N arrive as zeros and their columns are not stored)
 __device__ __forceinline__ int mma_n(int n_eff) { return (n_eff + 31) & ~31; }
 
-// bits of the largest finite relu(acc)^2 among a row's first n features
-__device__ __forceinline__ uint32_t relu2_amax(int n, const float (&acc)[COLS]) {
+// relu of a row's first n features in place (n a multiple of 16), and the bits of
+// the largest finite square.  Squaring keeps the order of what is not negative, so
+// the maximum is taken before it, as an integer, where Inf and NaN come out on top:
+// only then the squares are looked at one by one.
+__device__ __forceinline__ uint32_t relu_amax(int n, float (&acc)[COLS]) {
   uint32_t m = 0;
 #pragma unroll
+  for (int c = 0; c < COLS; c += 16) {
+    if (c >= n) break;
+#pragma unroll
+    for (int i = c; i < c + 16; i += 2) {
+      acc[i] = f8::relu_nan(acc[i]);
+      acc[i + 1] = f8::relu_nan(acc[i + 1]);
+      m = __vimax3_u32(m, f8::mag_bits(acc[i]), f8::mag_bits(acc[i + 1]));
+    }
+  }
+  const float top = __uint_as_float(m);
+  const uint32_t sq = f8::mag_bits(top * top);
+  if (m < f8::INF_BITS && sq < f8::INF_BITS) return sq;
+  m = 0;
+#pragma unroll
   for (int i = 0; i < COLS; ++i) {
-    const uint32_t b = f8::mag_bits(f8::relu2_nan(acc[i]));
-    m = max(m, b < f8::INF_BITS && i < n ? b : 0u);
+    const uint32_t b = f8::mag_bits(acc[i] * acc[i]);
+    if (i < n && b < f8::INF_BITS) m = max(m, b);
   }
   return m;
 }
@@ -197,7 +214,7 @@ __device__ __forceinline__ uint32_t relu2_amax(int n, const float (&acc)[COLS]) 
 // exist; n: features that exist (a multiple of 16).
 template <int OUT>
 __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, int f0, int n,
-                                            const float (&acc)[COLS], uint4* stage, int lane) {
+                                            float (&acc)[COLS], uint4* stage, int lane) {
   constexpr bool F32 = OUT == OUT_F32 || OUT == OUT_ADD_F32 || OUT == OUT_COMBINE;
   constexpr int PER = F32 ? 4 : (OUT == OUT_BF16 ? 8 : 16);   // features of a 16-byte word
   constexpr int PASSES = COLS / (8 * PER);
@@ -209,7 +226,7 @@ __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, i
     w = g.perm_w[mine];
   }
   if constexpr (OUT == OUT_RELU2_F8) {
-    const int e = f8::scale_exp(relu2_amax(n, acc));
+    const int e = f8::scale_exp(relu_amax(n, acc));
     w = f8::pow2(-e);
     if (lane < rows) g.out_scales[(size_t)mine * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
   }
@@ -229,7 +246,7 @@ __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, i
       } else {
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = f8::relu2_nan(acc[c + i]);
+        for (int i = 0; i < 16; ++i) v[i] = acc[c + i] * acc[c + i];
         word = f8::encode16(v, w);
       }
       stage[lane * 8 + (j ^ (lane & 7))] = word;

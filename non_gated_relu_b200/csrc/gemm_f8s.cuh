@@ -9,11 +9,13 @@
 // stages 16 KB of weights and NT / 8 KB of activations, its MMAs (M = 128, N =
 // NT, four of K = 32 from zero) take a fraction of the time the weights take to
 // arrive, and the rate is that of memory as long as enough bytes are under way:
-// two CTAs per SM (one for NT = 128), each with about 100 KB of stages.  As in
+// two CTAs per SM, each with about 100 KB of stages (one CTA of 192 KB, as 128
+// rows a tile would need, drew 3.7 TB/s where two draw 6).  As in
 // the pair kernel each K block is its own accumulator, four in turn, drained
 // into registers times its scales by eight warps (warp w: weight rows of quarter
 // w mod 4, half of the columns); the weight scale is one number per block and the
-// row scales are held by the lanes, one column each.
+// row scales are held by the lanes, one column each, and pass through shared
+// memory.
 //
 // A launch that follows this call's own quantization starts on its first stages'
 // weights before it waits for it (they were there before), which covers launch
@@ -67,7 +69,7 @@ struct Shape {
   static constexpr int TMEM_COLS = NBUF * NT;
   static constexpr int NBAR = 2 * STAGES + 2 * NBUF + 1 + 4;
   static constexpr int CODES = NT * 144;              // [NT][128] codes, rows 144 bytes apart
-  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + CODES + 4 * NT * 4 + NBAR * 8 + 16;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + CODES + 8 * NT * 4 + NBAR * 8 + 16;
   static_assert(SMEM * CTAS <= 227 * 1024, "shared memory of an SM");
   static_assert(TMEM_COLS * CTAS <= 512 && TMEM_COLS >= 32, "tensor memory");
   static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
@@ -115,7 +117,8 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   uint8_t* const base_ptr = smem_raw + (base - raw);
   uint8_t* const codes = base_ptr + STAGES * S::STAGE_BYTES;                  // [NT][144]
   uint32_t* const amax = reinterpret_cast<uint32_t*>(codes + S::CODES);       // [4][NT]
-  const uint32_t bar0 = base + STAGES * S::STAGE_BYTES + S::CODES + 4 * NT * 4;
+  float* const col_scales = reinterpret_cast<float*>(amax + 4 * NT);          // [DRAINS][NC]
+  const uint32_t bar0 = base + STAGES * S::STAGE_BYTES + S::CODES + 8 * NT * 4;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF);
   // per column half: maxima written, codes written
   auto half_bar = [&](int h, int w) { return bar0 + 8u * (2 * STAGES + 2 * NBUF + 1 + 2 * h + w); };
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(codes + S::CODES + 4 * NT * 4 + S::NBAR * 8);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(codes + S::CODES + 8 * NT * 4 + S::NBAR * 8);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
     // ---------------- drain: 32 weight rows x NC columns per warp ----------------
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * NC);
+    float* const scales = col_scales + (warp - 2) * NC;
     uint32_t use = 0, tiles_done = 0;
     bool ok = true;
     for (; ok && t.m < num_m; t.next(n_blocks, step_m, step_nb)) {
@@ -286,9 +290,13 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       for (int c = 0; c < NC; ++c) acc[c] = 0.f;
       for (int kb = 0; kb < nk; ++kb, ++use) {
         const uint32_t a = use % NBUF;
-        float s[CL];
+        // the columns' scales, read back four to a load (one shuffle a column takes
+        // an SM's shuffle unit longer than the weights of 64 columns need to arrive)
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < CL; ++i) s[i] = sx[i] * sw;
+        for (int i = 0; i < CL; ++i)
+          if (lane + 32 * i < NC) scales[lane + 32 * i] = sx[i] * sw;
+        __syncwarp();
         if (kb + 1 < nk) {
           sw = __ldg(ws + kb + 1);
 #pragma unroll
@@ -305,8 +313,13 @@ __global__ void __launch_bounds__(THREADS, CTAS)
         __syncwarp();
         if (lane == 0) f8g::arrive_relaxed(tempty_bar(a));
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          acc[c] = fmaf(__shfl_sync(0xffffffffu, s[c / 32], c & 31), __uint_as_float(v[c]), acc[c]);
+        for (int c = 0; c < NC; c += 4) {
+          const float4 s = *reinterpret_cast<const float4*>(scales + c);
+          acc[c] = fmaf(s.x, __uint_as_float(v[c]), acc[c]);
+          acc[c + 1] = fmaf(s.y, __uint_as_float(v[c + 1]), acc[c + 1]);
+          acc[c + 2] = fmaf(s.z, __uint_as_float(v[c + 2]), acc[c + 2]);
+          acc[c + 3] = fmaf(s.w, __uint_as_float(v[c + 3]), acc[c + 3]);
+        }
       }
       if (!ok) break;
       const int cols = min(NC, ent.z - half * NC);         // <= 0: none in this half
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          const float v = f8::nan_if_inf(acc[c] * f8::pow2(-__shfl_sync(0xffffffffu, ex[c / 32], c & 31)));
+          const float v = f8::scaled(acc[c], f8::pow2(-__shfl_sync(0xffffffffu, ex[c / 32], c & 31)));
           codes[(half * NC + c) * 144 + quarter * 32 + lane] = (uint8_t)f8::encode2(v, v);
         }
         __syncwarp();

@@ -107,8 +107,7 @@ static nh_status launch_f8_swap(const F8Call& c, int dev, cudaStream_t st) {
   switch (c.tile_rows) {
     case 16: return launch_f8_swap_as<16, 5, 2>(c, dev, st);
     case 32: return launch_f8_swap_as<32, 5, 2>(c, dev, st);
-    case 64: return launch_f8_swap_as<64, 4, 2>(c, dev, st);
-    default: return launch_f8_swap_as<128, 6, 1>(c, dev, st);
+    default: return launch_f8_swap_as<64, 4, 2>(c, dev, st);
   }
 }
 

@@ -37,17 +37,25 @@ constexpr uint32_t INF_BITS = 0x7f800000u;
 
 // Two values times a power of two as a pair of codes (low byte first).  Scaled
 // finite values never pass 448, so only Inf and NaN give the NaN code.
+// (The conversion saturates: an Inf has to be made a NaN first.)
 __device__ __forceinline__ uint32_t encode2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ float nan_if_inf(float v) {
-  return mag_bits(v) >= INF_BITS ? __int_as_float(0x7fffffff) : v;
-}
+// v times a power of two; Inf becomes NaN (Inf * 0)
+__device__ __forceinline__ float scaled(float v, float inv) { return fmaf(v, inv, v * 0.0f); }
 
-// relu(v)^2 that keeps a NaN
-__device__ __forceinline__ float relu2_nan(float v) { return v < 0.f ? 0.f : v * v; }
+// relu(v) that keeps a NaN, and its square
+__device__ __forceinline__ float relu_nan(float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float relu2_nan(float v) {
+  const float r = relu_nan(v);
+  return r * r;
+}
 
 // 16 values of a row from global memory
 __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
@@ -95,7 +103,7 @@ __device__ __forceinline__ uint4 encode16(const float (&v)[16], float inv) {
   for (int i = 0; i < 4; ++i) {
     float s[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = nan_if_inf(v[4 * i + j] * inv);
+    for (int j = 0; j < 4; ++j) s[j] = scaled(v[4 * i + j], inv);
     w[i] = encode2(s[0], s[1]) | (encode2(s[2], s[3]) << 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);

@@ -191,7 +191,7 @@ def test_fp8_workspace_holds_codes_and_scales(T):
     L = nh.workspace_layout(cfg, T)
     rows = T * cfg.k
     assert L.x_direct == 0 and L.swap_ab == int(L.tile_rows < 256)
-    assert L.tile_rows in (16, 32, 64, 128, 256)
+    assert L.tile_rows in (16, 32, 64, 256)
     assert L.max_tiles >= -(-rows // L.tile_rows) + min(rows, cfg.E - 1)
     assert L.h - L.x_perm >= rows * (cfg.H + 4 * -(-cfg.H // 128))
     assert L.ready - L.h >= rows * (cfg.I + 4 * -(-cfg.I // 128))
