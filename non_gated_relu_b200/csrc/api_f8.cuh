@@ -78,14 +78,7 @@ nh_status nh_fp8_linear(int64_t T, int64_t N, int64_t K, const void* x, int32_t 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* xq = at<uint8_t>(ws, ALIGN);
   float* xs = at<float>(ws, ALIGN + f8_scales_at(T, K));
-  if (x_dtype == NH_BF16)
-    NH_TRY(launch_quantize(static_cast<const __nv_bfloat16*>(x), T, (int)K, xq, xs, nullptr, 0, dev, st));
-  else
-    NH_TRY(launch_quantize(static_cast<const float*>(x), T, (int)K, xq, xs, nullptr, 0, dev, st));
   F8Call c{};
-  c.x = xq;
-  c.xs = xs;
-  c.x_rows = T;
   c.w = w;
   c.n_exp = 1;
   c.rows = T;
@@ -94,8 +87,7 @@ nh_status nh_fp8_linear(int64_t T, int64_t N, int64_t K, const void* x, int32_t 
   c.out_kind = y_dtype == NH_BF16 ? F8_BF16 : F8_F32;
   c.out = y;
   c.status = static_cast<int*>(ws);
-  c.early_w = true;   // the launch before is this call's quantization
-  return run_f8(c, dev, st);
+  return run_f8_dense(c, x, x_dtype == NH_BF16, xq, xs, false, dev, st);
 }
 
 // The two projections of the routed experts on the workspace.  `follows`: the
@@ -122,7 +114,11 @@ static nh_status f8_experts_up(const Plan& p, int64_t T, const void* x, const nh
   c.tile_rows = L.tile_rows;
   c.status = at<int>(ws, L.status);
   c.early_w = true;   // the launch before is this call's quantization
-  return run_f8_up(c, f8_hidden(at<void>(ws, L.h), p.rows, p.I), dev, st);
+  const F8Hidden h = f8_hidden(at<void>(ws, L.h), p.rows, p.I);
+  c.out_kind = F8_RELU2;
+  c.out = h.codes;
+  c.out_scales = h.scales;
+  return run_f8(c, dev, st);
 }
 
 static nh_status f8_experts_down(const Plan& p, const nh_fp8_weight* w, void* ws, float* y_acc,
@@ -217,27 +213,31 @@ static nh_status f8_shared(const nh_moe_config* cfg, int64_t T, const void* x,
   uint8_t* xq = at<uint8_t>(ws, ALIGN);
   float* xs = at<float>(ws, ALIGN + f8_scales_at(T, p.H));
   const F8Hidden h = f8_hidden(at<void>(ws, ALIGN + f8_rows_bytes(T, p.H)), T, p.S);
-  NH_TRY(launch_quantize(static_cast<const __nv_bfloat16*>(x), T, p.H, xq, xs, nullptr, 0, dev, st));
-  F8Call c{};
-  c.x = xq;
-  c.xs = xs;
-  c.x_rows = T;
-  c.w = w_su;
-  c.n_exp = 1;
-  c.rows = T;
-  c.N = p.S;
-  c.K = p.H;
-  c.status = status;
-  c.early_w = true;   // the launch before is this call's quantization
-  NH_TRY(run_f8_up(c, h, dev, st));
-  c.x = h.codes;
-  c.xs = h.scales;
-  c.w = w_sd;
-  c.N = p.H;
-  c.K = p.S;
-  c.out_kind = store ? F8_F32 : F8_ADD;
-  c.out = y_acc;
-  return run_f8(c, dev, st);
+  F8Call up{};
+  up.w = w_su;
+  up.n_exp = 1;
+  up.rows = T;
+  up.N = p.S;
+  up.K = p.H;
+  up.status = status;
+  // the GEMV leaves relu^2 in float32, to be quantized by what follows; the tiles'
+  // ends quantize it themselves
+  const bool gemv = f8_gemv_rows(up);
+  up.out_kind = F8_RELU2;
+  up.out = gemv ? static_cast<void*>(h.f32) : h.codes;
+  up.out_scales = h.scales;
+  NH_TRY(run_f8_dense(up, x, true, xq, xs, false, dev, st));
+  F8Call down = up;
+  down.w = w_sd;
+  down.N = p.H;
+  down.K = p.S;
+  down.out_kind = store ? F8_F32 : F8_ADD;
+  down.out = y_acc;
+  if (gemv) return run_f8_dense(down, h.f32, false, h.codes, h.scales, true, dev, st);
+  down.x = h.codes;
+  down.xs = h.scales;
+  down.x_rows = T;
+  return run_f8(down, dev, st);
 }
 
 nh_status nh_moe_shared_fp8(const nh_moe_config* cfg, int64_t T, const void* x,

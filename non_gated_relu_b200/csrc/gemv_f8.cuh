@@ -11,6 +11,14 @@
 // bytes is k-slot i for weights and activations alike.  Each block's product
 // starts from zero and enters the running sum times its two scales; the warps'
 // sums are added in warp order, so a result does not depend on scheduling.
+//
+// Up to 8 rows the activations come unquantized: the four lanes that hold a
+// token's block of 128 find its maximum with two shuffles and encode their words
+// in registers, every CTA for itself, instead of a launch before this one.  3712 x
+// 2688, 1 row: a call from the host takes 10 us in one launch and 15 in two; in a
+// CUDA graph it is 5.1 against 4.0, because the second launch can ask for its
+// weights ahead (asking for the values ahead, fewer blocks in flight and CTAs of
+// four warps were all slower).
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -30,8 +38,8 @@ enum Out : int {
 };
 
 struct Args {
-  const uint8_t* x;        // codes [rows, K]
-  const float* xs;         // scales [rows, KB]
+  const void* x;           // codes, or values, [rows, K]
+  const float* xs;         // scales of codes [rows, KB]
   const uint8_t* w;        // codes [N, K]
   const float* ws;         // scales [ceil(N / 128), KB]
   int rows;                // at most NT
@@ -58,10 +66,39 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
   return v;
 }
 
-// NT: rows, padded (8, 16, 32); U: K blocks of a warp in flight
-template <int NT, int U>
-__global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
+// One lane's 16 values at p, or zeros, as codes of a block whose other values lie
+// in the lanes next to it; `e` is the exponent of the block's scale.
+template <typename Tx>
+__device__ __forceinline__ void quantize_block(const Tx* p, bool in0, bool in1, uint4& q0, uint4& q1,
+                                               int& e) {
+  float v0[16], v1[16];
+  if (in0) {
+    f8::load16(p, v0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v0[i] = 0.f;
+  }
+  if (in1) {
+    f8::load16(p + 64, v1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v1[i] = 0.f;
+  }
+  uint32_t m = max(f8::amax16(v0), f8::amax16(v1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  e = f8::scale_exp(m);
+  q0 = f8::encode16(v0, f8::pow2(-e));
+  q1 = f8::encode16(v1, f8::pow2(-e));
+}
+
+// NT: rows, padded (8, 16, 32); U: K blocks of a warp in flight; Tx: uint8_t for
+// codes, else the type of the values (NT = 8)
+template <int NT, int U, typename Tx>
+__global__ void __launch_bounds__(WARPS * 32, 2) f8_gemv(const Args a) {
   constexpr int NB = NT / 8;
+  constexpr bool RAW = sizeof(Tx) > 1;
+  static_assert(!RAW || NT == 8, "values are quantized for one tile of 8 tokens");
   __shared__ float red[WARPS][MT][NT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
@@ -88,11 +125,11 @@ __global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
   // x rows of this lane's fragment columns (token gq of each n-tile) and of its
   // accumulator columns (tokens 2 tq, 2 tq + 1); rows past the last repeat it and
   // are not stored
-  const uint8_t* xp[NB];
+  const Tx* xp[NB];
   const float* sp[NB][2];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    xp[j] = a.x + (size_t)min(8 * j + gq, a.rows - 1) * a.K;
+    xp[j] = static_cast<const Tx*>(a.x) + (size_t)min(8 * j + gq, a.rows - 1) * a.K;
     sp[j][0] = a.xs + (size_t)min(8 * j + 2 * tq, a.rows - 1) * a.KB;
     sp[j][1] = a.xs + (size_t)min(8 * j + 2 * tq + 1, a.rows - 1) * a.KB;
   }
@@ -121,15 +158,26 @@ __global__ void __launch_bounds__(WARPS * 32) f8_gemv(const Args a) {
       for (int j = 0; j < NB; ++j) {
         if (8 * j >= a.rows) break;
         float d[4] = {0.f, 0.f, 0.f, 0.f};
+        const int off = b * 128 + tq * 16;
+        uint4 xv[2];
+        float s0, s1;
+        if constexpr (RAW) {
+          int e;
+          quantize_block(xp[j] + off, off < a.K, off + 64 < a.K, xv[0], xv[1], e);
+          s0 = f8::pow2(__shfl_sync(0xffffffffu, e, 8 * tq)) * sw[u];
+          s1 = f8::pow2(__shfl_sync(0xffffffffu, e, 8 * tq + 4)) * sw[u];
+        } else {
+          xv[0] = off < a.K ? *reinterpret_cast<const uint4*>(xp[j] + off) : zero;
+          xv[1] = off + 64 < a.K ? *reinterpret_cast<const uint4*>(xp[j] + off + 64) : zero;
+          s0 = sp[j][0][b] * sw[u];
+          s1 = sp[j][1][b] * sw[u];
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int off = b * 128 + h * 64 + tq * 16;
-          const uint4 xv = off < a.K ? *reinterpret_cast<const uint4*>(xp[j] + off) : zero;
           const uint4 p = wv[u][2 * h], q = wv[u][2 * h + 1];
-          mma_e4m3(d, p.x, q.x, p.y, q.y, xv.x, xv.y);
-          mma_e4m3(d, p.z, q.z, p.w, q.w, xv.z, xv.w);
+          mma_e4m3(d, p.x, q.x, p.y, q.y, xv[h].x, xv[h].y);
+          mma_e4m3(d, p.z, q.z, p.w, q.w, xv[h].z, xv[h].w);
         }
-        const float s0 = sp[j][0][b] * sw[u], s1 = sp[j][1][b] * sw[u];
         acc[j][0] = fmaf(s0, d[0], acc[j][0]);
         acc[j][1] = fmaf(s1, d[1], acc[j][1]);
         acc[j][2] = fmaf(s0, d[2], acc[j][2]);

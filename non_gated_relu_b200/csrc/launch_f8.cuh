@@ -46,9 +46,11 @@ struct F8Call {
   bool early_w;
 };
 
-static nh_status launch_f8_gemv(const F8Call& c, cudaStream_t st) {
+// x: null for the call's codes, else values of x_type (at most F8_RAW_ROWS rows)
+static nh_status launch_f8_gemv(const F8Call& c, cudaStream_t st, const void* x = nullptr,
+                                bool x_bf16 = false) {
   f8v::Args a{};
-  a.x = c.x;
+  a.x = x ? x : c.x;
   a.xs = c.xs;
   a.w = c.w->codes;
   a.ws = c.w->scales;
@@ -66,9 +68,10 @@ static nh_status launch_f8_gemv(const F8Call& c, cudaStream_t st) {
   a.out = c.out;
   a.early_w = c.early_w ? 1 : 0;
   const dim3 g((unsigned)(c.N / f8v::MT)), b(f8v::WARPS * 32);
-  if (c.rows <= 8) return launch_k("f8_gemv", f8v::f8_gemv<8, 3>, g, b, 0, st, a);
-  if (c.rows <= 16) return launch_k("f8_gemv", f8v::f8_gemv<16, 2>, g, b, 0, st, a);
-  return launch_k("f8_gemv", f8v::f8_gemv<32, 2>, g, b, 0, st, a);
+  if (x && x_bf16) return launch_k("f8_gemv", f8v::f8_gemv<8, 3, __nv_bfloat16>, g, b, 0, st, a);
+  if (x) return launch_k("f8_gemv", f8v::f8_gemv<8, 3, float>, g, b, 0, st, a);
+  if (c.rows <= 16) return launch_k("f8_gemv", f8v::f8_gemv<16, 2, uint8_t>, g, b, 0, st, a);
+  return launch_k("f8_gemv", f8v::f8_gemv<32, 2, uint8_t>, g, b, 0, st, a);
 }
 
 // the routed experts' products with weights on the MMA M side
@@ -200,14 +203,22 @@ static F8Hidden f8_hidden(void* base, int64_t R, int64_t C) {
           reinterpret_cast<float*>(b + f8_rows_bytes(R, C))};
 }
 
-// up projection with relu^2, its result quantized: c.out and c.out_scales are
-// set here from `h`
-static nh_status run_f8_up(F8Call c, const F8Hidden& h, int dev, cudaStream_t st) {
-  c.out_kind = F8_RELU2;
-  const bool gemv = f8_gemv_rows(c);
-  c.out = gemv ? static_cast<void*>(h.f32) : h.codes;
-  c.out_scales = h.scales;
-  NH_TRY(run_f8(c, dev, st));
-  if (!gemv) return NH_OK;
-  return launch_quantize(h.f32, c.rows, c.N, h.codes, h.scales, nullptr, 0, dev, st);
+// A dense product of unquantized rows: in one launch up to F8_RAW_ROWS of them,
+// else quantized to xq, xs first.  early_raw: the previous launch in the stream
+// belongs to the same call.
+static nh_status run_f8_dense(F8Call c, const void* x, bool bf16, uint8_t* xq, float* xs,
+                              bool early_raw, int dev, cudaStream_t st) {
+  if (c.rows <= F8_RAW_ROWS) {
+    c.early_w = early_raw;
+    return launch_f8_gemv(c, st, x, bf16);
+  }
+  if (bf16)
+    NH_TRY(launch_quantize(static_cast<const __nv_bfloat16*>(x), c.rows, c.K, xq, xs, nullptr, 0, dev, st));
+  else
+    NH_TRY(launch_quantize(static_cast<const float*>(x), c.rows, c.K, xq, xs, nullptr, 0, dev, st));
+  c.x = xq;
+  c.xs = xs;
+  c.x_rows = c.rows;
+  c.early_w = true;
+  return run_f8(c, dev, st);
 }

@@ -83,6 +83,7 @@ constexpr int ROUTE_PERMUTE_MAX_E = 256;
 constexpr int ROUTE_PERMUTE_SMEM_MAX = (16 * 256 + 256 + 3 * 32 * 32) * 4;
 
 constexpr int F8_GEMV_ROWS = 32;   // rows up to which dense FP8 products run as GEMVs
+constexpr int F8_RAW_ROWS = 8;     // and up to which those quantize their rows themselves
 
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
