@@ -21,8 +21,8 @@ nh_status nh_fp8_quantize(int64_t T, int64_t K, const void* x, int32_t dtype, ui
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == NH_BF16)
     return launch_quantize(static_cast<const __nv_bfloat16*>(x), T, (int)K, codes, scales, nullptr, 0,
-                           dev, st);
-  return launch_quantize(static_cast<const float*>(x), T, (int)K, codes, scales, nullptr, 0, dev, st);
+                           st);
+  return launch_quantize(static_cast<const float*>(x), T, (int)K, codes, scales, nullptr, 0, st);
 }
 
 nh_status nh_fp8_quantize_weight(int64_t n_mat, int64_t rows, int64_t cols, const void* w,
@@ -98,7 +98,7 @@ static nh_status f8_experts_up(const Plan& p, int64_t T, const void* x, const nh
   uint8_t* xq = at<uint8_t>(ws, L.x_perm);
   float* xs = at<float>(ws, L.x_perm + f8_scales_at(p.rows, p.H));
   NH_TRY(launch_quantize(static_cast<const __nv_bfloat16*>(x), T, p.H, xq, xs,
-                         at<int32_t>(ws, L.inv_row), p.k, dev, st));
+                         at<int32_t>(ws, L.inv_row), p.k, st));
   F8Call c{};
   c.x = xq;
   c.xs = xs;

@@ -244,10 +244,10 @@ __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, i
         word = make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
                           pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
       } else {
-        float v[16];
+        f8::F32x16 sq;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = acc[c + i] * acc[c + i];
-        word = f8::encode16(v, w);
+        for (int i = 0; i < 16; ++i) sq.v[i] = acc[c + i] * acc[c + i];
+        word = f8::encode16(sq, w);
       }
       stage[lane * 8 + (j ^ (lane & 7))] = word;
     }

@@ -71,19 +71,9 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
 template <typename Tx>
 __device__ __forceinline__ void quantize_block(const Tx* p, bool in0, bool in1, uint4& q0, uint4& q1,
                                                int& e) {
-  float v0[16], v1[16];
-  if (in0) {
-    f8::load16(p, v0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v0[i] = 0.f;
-  }
-  if (in1) {
-    f8::load16(p + 64, v1);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v1[i] = 0.f;
-  }
+  typename f8::Raw<Tx>::type v0, v1;
+  f8::load16(p, in0, v0);
+  f8::load16(p + 64, in1, v1);
   uint32_t m = max(f8::amax16(v0), f8::amax16(v1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));

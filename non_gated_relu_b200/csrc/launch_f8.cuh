@@ -182,12 +182,12 @@ static nh_status run_f8(const F8Call& c, int dev, cudaStream_t st) {
 // Quantize R rows of C values; with inv_row each to its k permuted rows.
 template <typename Tin>
 static nh_status launch_quantize(const Tin* x, int64_t R, int C, uint8_t* codes, float* scales,
-                                 const int32_t* inv_row, int k, int dev, cudaStream_t st) {
+                                 const int32_t* inv_row, int k, cudaStream_t st) {
   const int64_t kb = f8_blocks(C), units = R * kb;
   if (units == 0) return NH_OK;
   if (units > 0x7fffffff) return fail(NH_ERR_UNSUPPORTED, "quantization of %lld blocks", (long long)units);
-  return launch_k("quantize_rows", f8::quantize_rows<Tin>, dim3(grid_for(units, 32, dev)), dim3(256),
-                  0, st, x, (uint32_t)units, C, (int)kb, codes, scales, inv_row, k);
+  return launch_k("quantize_rows", f8::quantize_rows<Tin>, dim3((unsigned)((units + 31) / 32)),
+                  dim3(256), 0, st, x, (uint32_t)units, C, (int)kb, codes, scales, inv_row, k);
 }
 
 // Dense rows that a kernel left in float32 behind their quantized form
@@ -213,9 +213,9 @@ static nh_status run_f8_dense(F8Call c, const void* x, bool bf16, uint8_t* xq, f
     return launch_f8_gemv(c, st, x, bf16);
   }
   if (bf16)
-    NH_TRY(launch_quantize(static_cast<const __nv_bfloat16*>(x), c.rows, c.K, xq, xs, nullptr, 0, dev, st));
+    NH_TRY(launch_quantize(static_cast<const __nv_bfloat16*>(x), c.rows, c.K, xq, xs, nullptr, 0, st));
   else
-    NH_TRY(launch_quantize(static_cast<const float*>(x), c.rows, c.K, xq, xs, nullptr, 0, dev, st));
+    NH_TRY(launch_quantize(static_cast<const float*>(x), c.rows, c.K, xq, xs, nullptr, 0, st));
   c.x = xq;
   c.xs = xs;
   c.x_rows = c.rows;

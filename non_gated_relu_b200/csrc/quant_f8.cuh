@@ -57,53 +57,80 @@ __device__ __forceinline__ float relu2_nan(float v) {
   return r * r;
 }
 
-// 16 values of a row from global memory
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
+// 16 values of a row as they lie in global memory
+struct Bf16x16 {
+  uint32_t w[8];
+};
+struct F32x16 {
+  float v[16];
+};
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, bool in, Bf16x16& r) {
   const uint4* q = reinterpret_cast<const uint4*>(p);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint4 u = q[h];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
-      v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    const uint4 u = in ? q[h] : make_uint4(0, 0, 0, 0);
+    r.w[4 * h] = u.x;
+    r.w[4 * h + 1] = u.y;
+    r.w[4 * h + 2] = u.z;
+    r.w[4 * h + 3] = u.w;
   }
 }
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+__device__ __forceinline__ void load16(const float* p, bool in, F32x16& r) {
   const float4* q = reinterpret_cast<const float4*>(p);
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
-    const float4 f = q[h];
-    v[4 * h] = f.x;
-    v[4 * h + 1] = f.y;
-    v[4 * h + 2] = f.z;
-    v[4 * h + 3] = f.w;
+    const float4 f = in ? q[h] : make_float4(0.f, 0.f, 0.f, 0.f);
+    r.v[4 * h] = f.x;
+    r.v[4 * h + 1] = f.y;
+    r.v[4 * h + 2] = f.z;
+    r.v[4 * h + 3] = f.w;
   }
 }
+__device__ __forceinline__ float value(const Bf16x16& r, int i) {
+  return __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+}
+__device__ __forceinline__ float value(const F32x16& r, int i) { return r.v[i]; }
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> { using type = Bf16x16; };
+template <> struct Raw<float> { using type = F32x16; };
 
-// bits of the largest magnitude of 16 values; Inf and NaN are left out where
-// there are any
-__device__ __forceinline__ uint32_t amax16(const float (&v)[16]) {
+// Bits of the largest magnitude of 16 values, as integers (two bf16 at a time);
+// Inf and NaN come out on top, and only where there are any they are left out one
+// by one.
+__device__ __forceinline__ uint32_t amax_any(const Bf16x16& r) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, mag_bits(v[i]));
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, r.w[i] & 0x7fff7fffu);
+  return max(m & 0xffff0000u, m << 16);
+}
+__device__ __forceinline__ uint32_t amax_any(const F32x16& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) m = __vimax3_u32(m, mag_bits(r.v[i]), mag_bits(r.v[i + 1]));
+  return m;
+}
+template <typename R>
+__device__ __forceinline__ uint32_t amax16(const R& r) {
+  uint32_t m = amax_any(r);
   if (m >= INF_BITS) {
     m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, mag_bits(v[i]) < INF_BITS ? mag_bits(v[i]) : 0u);
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t b = mag_bits(value(r, i));
+      m = max(m, b < INF_BITS ? b : 0u);
+    }
   }
   return m;
 }
 
-__device__ __forceinline__ uint4 encode16(const float (&v)[16], float inv) {
+template <typename R>
+__device__ __forceinline__ uint4 encode16(const R& r, float inv) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float s[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = scaled(v[4 * i + j], inv);
+    for (int j = 0; j < 4; ++j) s[j] = scaled(value(r, 4 * i + j), inv);
     w[i] = encode2(s[0], s[1]) | (encode2(s[2], s[3]) << 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -120,19 +147,13 @@ __global__ void __launch_bounds__(256) quantize_rows(const Tin* __restrict__ x, 
   pdl_wait();
   pdl_trigger();
   const int sub = threadIdx.x & 7;
-  const uint32_t stride = gridDim.x * (blockDim.x >> 3);
-  const uint32_t first = blockIdx.x * (blockDim.x >> 3) + (threadIdx.x >> 3);
+  const uint32_t u = blockIdx.x * (blockDim.x >> 3) + (threadIdx.x >> 3);
   const unsigned group = 0xffu << (threadIdx.x & 24);
-  for (uint32_t u = first; u < units; u += stride) {
+  if (u < units) {
     const uint32_t row = u / (uint32_t)KB, b = u - row * (uint32_t)KB;
     const int col = (int)b * BLK + sub * 16;
-    float v[16];
-    if (col < K) {
-      load16(x + (size_t)row * K + col, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    }
+    typename Raw<Tin>::type v;
+    load16(x + (size_t)row * K + col, col < K, v);
     uint32_t m = amax16(v);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(group, m, o));
@@ -167,16 +188,11 @@ __global__ void __launch_bounds__(256) quantize_blocks(const Tin* __restrict__ w
   const int r = (in / CB) * BLK + (threadIdx.x >> 1);
   const int c0 = (in % CB) * BLK + (threadIdx.x & 1) * 64;
   const size_t at = ((size_t)mat * rows + r) * cols;
-  float v[4][16];
+  typename Raw<Tin>::type v[4];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (r < rows && c0 + 16 * i < cols) {
-      load16(w + at + c0 + 16 * i, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[i][j] = 0.f;
-    }
+    load16(w + at + c0 + 16 * i, r < rows && c0 + 16 * i < cols, v[i]);
     m = max(m, amax16(v[i]));
   }
   m = __reduce_max_sync(0xffffffffu, m);
