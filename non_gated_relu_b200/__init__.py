@@ -10,6 +10,14 @@ Low level (same names as the C ABI, minus the ``nh_moe_`` prefix):
 ``check_device``, ``workspace_size``, ``workspace_layout``,
 ``shared_workspace_size``, ``validate``, ``selftest_timeout``.
 
+From router logits: ``gate`` (sigmoid or softmax scores, bias, groups, top-k) and
+its gradient ``gate_backward``; ``route_scored`` runs the router and the gate.
+
+FP8 (E4M3 with a scale per block of 128): ``fp8_quantize`` (rows),
+``fp8_quantize_weight``, ``fp8_weight``, ``fp8_linear``, and ``forward_fp8``,
+``experts_up_fp8`` / ``experts_down_fp8``, ``shared_fp8`` / ``shared_store_fp8``
+for a config with ``weight_format`` "fp8".
+
 Block level: :class:`NemotronHMoE` (``block.py``) holds the weights and
 buffers and runs one block call on two streams (optionally as a CUDA graph).
 """
@@ -421,6 +429,18 @@ def _args(*specs):
     return out
 
 
+def _ws_arg(name, ws):
+    """(pointer, bytes) of a workspace tensor on the current device"""
+    ty = _types()
+    if not isinstance(ws, ty.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(ws).__name__}")
+    if not ws.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to libnhmoe must be contiguous")
+    if ws.get_device() != ty.current_device():
+        raise ValueError(f"{name}: on {ws.device}, not on the current CUDA device")
+    return ws.data_ptr() or None, ws.numel() * ws.element_size()
+
+
 def gate_config(n_routed_experts, num_experts_per_tok, n_group=1, topk_group=1,
                 norm_topk_prob=True, routed_scaling_factor=1.0, scoring_func="sigmoid",
                 group_score="max", dtype="f32") -> GateConfig:
@@ -463,12 +483,19 @@ def gate_backward(cfg: GateConfig, logits, topk_idx, d_topk_w, d_logits, stream=
 
 def route_scored(cfg, scoring_func, x, w_router, bias, topk_idx, topk_w, ws, stream=None):
     """route with the scores of scoring_func ("sigmoid" or "softmax")."""
-    c = config_from(cfg)
+    c, ty = config_from(cfg), _types()
     if scoring_func not in _SCORE_FUNCS:
         raise ValueError(f"unknown scoring_func {scoring_func!r}")
-    _check(load().nh_moe_route_scored(ctypes.byref(c), _SCORE_FUNCS[scoring_func], x.shape[0],
-                                      _p(x), _p(w_router), _p(bias), _p(topk_idx), _p(topk_w),
-                                      _p(ws), _nbytes(ws), _stream(stream)))
+    T, E, k = x.shape[0], c.n_routed_experts, c.num_experts_per_tok
+    specs = [("x", x, ty.bf16 if c.dtype == NH_BF16 else ty.f32, (T, c.hidden_size)),
+             ("w_router", w_router, ty.f32, (E, c.hidden_size)),
+             ("topk_idx", topk_idx, ty.i32, (T, k)), ("topk_w", topk_w, ty.f32, (T, k))]
+    if bias is not None:
+        specs.append(("bias", bias, ty.f32, (E,)))
+    ptrs = _args(*specs)
+    _check(load().nh_moe_route_scored(ctypes.byref(c), _SCORE_FUNCS[scoring_func], T, ptrs[0],
+                                      ptrs[1], ptrs[4] if bias is not None else None, ptrs[2],
+                                      ptrs[3], *_ws_arg("ws", ws), _stream(stream)))
 
 
 def fp8_weight(codes, scales) -> Fp8Weight:
@@ -537,7 +564,7 @@ def fp8_linear(x, w: Fp8Weight, y, ws, stream=None):
     N = y.shape[1]
     ref = _fp8("w", w, (1, N, K))
     px, py = _args(("x", x, ty.act, (T, K)), ("y", y, ty.act, (T, N)))
-    _check(load().nh_fp8_linear(T, N, K, px, _dt(x), ref, py, _dt(y), _p(ws), _nbytes(ws),
+    _check(load().nh_fp8_linear(T, N, K, px, _dt(x), ref, py, _dt(y), *_ws_arg("ws", ws),
                                 _stream(stream)))
 
 
@@ -558,7 +585,7 @@ def forward_fp8(cfg, x, w_up: Fp8Weight, w_down: Fp8Weight, ws, y_acc, stream=No
     T, px, py = _f8_args(c, x, y_acc)
     E, H, I = c.n_routed_experts, c.hidden_size, c.moe_intermediate_size
     _check(load().nh_moe_forward_fp8(ctypes.byref(c), T, px, _fp8("w_up", w_up, (E, I, H)),
-                                     _fp8("w_down", w_down, (E, H, I)), _p(ws), _nbytes(ws), py,
+                                     _fp8("w_down", w_down, (E, H, I)), *_ws_arg("ws", ws), py,
                                      _stream(stream)))
 
 
@@ -566,8 +593,8 @@ def experts_up_fp8(cfg, x, w_up: Fp8Weight, ws, stream=None):
     c = config_from(cfg)
     T, px, _ = _f8_args(c, x, None)
     shape = (c.n_routed_experts, c.moe_intermediate_size, c.hidden_size)
-    _check(load().nh_moe_experts_up_fp8(ctypes.byref(c), T, px, _fp8("w_up", w_up, shape), _p(ws),
-                                        _nbytes(ws), _stream(stream)))
+    _check(load().nh_moe_experts_up_fp8(ctypes.byref(c), T, px, _fp8("w_up", w_up, shape),
+                                        *_ws_arg("ws", ws), _stream(stream)))
 
 
 def experts_down_fp8(cfg, T: int, w_down: Fp8Weight, ws, y_acc, stream=None):
@@ -576,8 +603,8 @@ def experts_down_fp8(cfg, T: int, w_down: Fp8Weight, ws, y_acc, stream=None):
     if y_acc.shape[0] != T:
         raise ValueError(f"y_acc: expected {T} rows, got {y_acc.shape[0]}")
     shape = (c.n_routed_experts, c.hidden_size, c.moe_intermediate_size)
-    _check(load().nh_moe_experts_down_fp8(ctypes.byref(c), T, _fp8("w_down", w_down, shape), _p(ws),
-                                          _nbytes(ws), py, _stream(stream)))
+    _check(load().nh_moe_experts_down_fp8(ctypes.byref(c), T, _fp8("w_down", w_down, shape),
+                                          *_ws_arg("ws", ws), py, _stream(stream)))
 
 
 def _shared_fp8(fn, cfg, x, w_su, w_sd, y_acc, ws_shared, stream):
@@ -585,7 +612,7 @@ def _shared_fp8(fn, cfg, x, w_su, w_sd, y_acc, ws_shared, stream):
     T, px, py = _f8_args(c, x, y_acc)
     H, S = c.hidden_size, c.moe_shared_expert_intermediate_size
     _check(fn(ctypes.byref(c), T, px, _fp8("w_shared_up", w_su, (1, S, H)),
-              _fp8("w_shared_down", w_sd, (1, H, S)), py, _p(ws_shared), _nbytes(ws_shared),
+              _fp8("w_shared_down", w_sd, (1, H, S)), py, *_ws_arg("ws_shared", ws_shared),
               _stream(stream)))
 
 

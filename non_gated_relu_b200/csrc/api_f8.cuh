@@ -3,7 +3,7 @@
 static nh_status check_f8_dims(int64_t rows, int64_t cols, const char* what) {
   if (rows < 0 || cols < 1) return fail(NH_ERR_INVALID_ARG, "%s: sizes must be positive", what);
   if (cols % 16) return fail(NH_ERR_UNSUPPORTED, "%s: needs a multiple of 16 features", what);
-  if (rows >= int64_t(1) << 31 || cols >= int64_t(1) << 30)
+  if (rows >= (int64_t(1) << 31) - 4096 || cols >= int64_t(1) << 30)
     return fail(NH_ERR_UNSUPPORTED, "%s: too large", what);
   return NH_OK;
 }

@@ -171,6 +171,48 @@ def test_linear_past_32_bits():
         check_product(y[part], ref.rows_values(x[part]), wv, K)
 
 
+@pytest.mark.parametrize("T", [0])
+def test_no_tokens(T):
+    gen = generator(1)
+    codes, scales = ref.make_weight(gen, 1, 64, 128)
+    x = torch.empty((0, 128), dtype=B16, device=DEV)
+    ws = torch.zeros(nh.fp8_linear_workspace_size(0, 64, 128), dtype=torch.uint8, device=DEV)
+    nh.fp8_linear(x, nh.fp8_weight(codes, scales), torch.empty((0, 64), dtype=B16, device=DEV), ws)
+    nh.fp8_quantize(x, torch.empty((0, 128), dtype=torch.uint8, device=DEV),
+                    torch.empty((0, 1), device=DEV))
+    cfg = config(0)
+    c = nh.config_from(cfg)
+    up, down = experts_case(cfg, gen)
+    ws = torch.zeros(nh.workspace_size(c, 0), dtype=torch.uint8, device=DEV)
+    x = torch.empty((0, cfg.H), dtype=B16, device=DEV)
+    y = torch.empty((0, cfg.H), device=DEV)
+    idx = torch.empty((0, cfg.k), dtype=torch.int32, device=DEV)
+    nh.permute(c, x, idx, torch.empty((0, cfg.k), device=DEV), ws)
+    nh.forward_fp8(c, x, nh.fp8_weight(*up), nh.fp8_weight(*down), ws, y)
+    assert nh.check_device(ws) == 0
+
+
+def test_tensors_off_the_device_are_refused():
+    codes, scales = ref.make_weight(generator(1), 1, 64, 128)
+    w = nh.fp8_weight(codes, scales)
+    x, y = torch.zeros((4, 128), dtype=B16, device=DEV), torch.zeros((4, 64), dtype=B16, device=DEV)
+    n = nh.fp8_linear_workspace_size(4, 64, 128)
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    for args in ((x.cpu(), w, y, ws), (x, w, y.cpu(), ws), (x, w, y, ws.cpu())):
+        with pytest.raises(ValueError):
+            nh.fp8_linear(*args)
+    with pytest.raises(ValueError):
+        nh.fp8_linear(x, nh.fp8_weight(*ref.make_weight(generator(1), 1, 64, 256)), y, ws)
+    with pytest.raises(ValueError):
+        nh.fp8_linear(x.t().contiguous().t(), w, y, ws)         # strided
+    with pytest.raises(ValueError):
+        nh.fp8_weight(codes.cpu(), scales)
+    with pytest.raises(nh.NHMoEError):
+        nh.fp8_linear(x, w, y, ws[: n - 256])
+    with pytest.raises(nh.NHMoEError):
+        nh.fp8_linear(torch.zeros(4 * 128 + 4, dtype=B16, device=DEV)[4:].view(4, 128), w, y, ws)
+
+
 def test_linear_non_finite_rows_stay_in_their_rows():
     gen = generator(9)
     for T in (5, 40, 300):
@@ -347,7 +389,7 @@ def routing(T, E, k, gen, skew=0.0):
     return idx, w
 
 
-@pytest.mark.parametrize("T", [1, 2, 8, 9, 16, 17, 32, 33, 65, 200, 300, 1500])
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 15, 16, 17, 32, 33, 65, 135, 200, 300, 515, 516, 1500])
 @pytest.mark.parametrize("kw", [
     dict(), dict(hidden_size=64, moe_intermediate_size=64),
     dict(hidden_size=704, moe_intermediate_size=576, n_routed_experts=8, num_experts_per_tok=2),
@@ -363,6 +405,29 @@ def test_experts(T, kw):
     b = check_experts(cfg, x, idx, w, up, down, split=True)
     # the same up to the order of the float32 adds of a token's k rows
     assert ((a - b).abs() <= 2.0 ** -22 * cfg.k * (a.abs().amax() + b.abs())).all()
+
+
+def test_experts_with_weights_past_32_bits():
+    """The last expert's codes lie past 2^32 bytes."""
+    cfg = config(5, hidden_size=4224, moe_intermediate_size=2048, n_routed_experts=512,
+                 n_group=1, topk_group=1, num_experts_per_tok=2)
+    gen = generator(31)
+
+    def big(rows, cols):
+        codes = torch.zeros((cfg.E, rows, cols), dtype=torch.uint8, device=DEV)
+        scales = torch.ones((cfg.E, -(-rows // 128), -(-cols // 128)), device=DEV)
+        for e in (0, 3, cfg.E - 1):
+            c, s = ref.make_weight(gen, 1, rows, cols)
+            codes[e], scales[e] = c[0].view(torch.uint8), s[0]
+        return codes, scales
+
+    up, down = big(cfg.I, cfg.H), big(cfg.H, cfg.I)
+    for T in (5, 300):
+        idx = torch.tensor([[cfg.E - 1, 3]], dtype=torch.int32, device=DEV).repeat(T, 1)
+        idx[1:3, 1] = 0
+        w = torch.rand((T, 2), generator=gen, device=DEV)
+        x = torch.randn((T, cfg.H), generator=gen, device=DEV).to(B16)
+        check_experts(cfg, x, idx, w, up, down)
 
 
 @pytest.mark.parametrize("T", [5, 32, 40, 700])
