@@ -312,6 +312,69 @@ __device__ __noinline__ int choose_f64(const Tin* row, const Args& a, double* c,
   return mine;
 }
 
+// The keys that reach `floor_key`, with their experts, into cand (32 of them at
+// most); returns how many there are.
+template <int PER>
+__device__ __forceinline__ int gather(const uint32_t (&key)[PER], uint32_t floor_key, int e0,
+                                      int lane, uint2* cand) {
+  int found = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const unsigned who = __ballot_sync(FULL, key[i] >= floor_key);
+    if (key[i] >= floor_key) {
+      const int at = found + __popc(who & ((1u << lane) - 1u));
+      if (at < 32) cand[at] = make_uint2(key[i], (uint32_t)(e0 + i));
+    }
+    found += __popc(who);
+  }
+  return found;
+}
+
+// A few candidates in the order of their 64-bit scores, one to a lane: pick j to
+// lane j.  A tenth of the time of choose_f64, whose lanes score all their experts
+// one after the other.
+template <int PER, typename Tin>
+__device__ __noinline__ int order_f64(const Tin* row, const Args& a, const uint2* cand, int n,
+                                      int lane) {
+  double top = 0.0, z = 1.0;
+  if (a.softmax) {
+    float l[PER];
+    load_row<PER>(row, a.E, lane, l);
+    float mine = l[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) mine = fmaxf(mine, l[i]);
+    const float t = warp_max(mine);
+    top = t == -INFINITY ? 0.0 : (double)t;
+    z = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) z += exp((double)l[i] - top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
+  }
+  int e = 0x7fffffff;
+  double c = -INFINITY;
+  if (lane < n) {
+    e = (int)cand[lane].y;
+    const double l = (double)clean(to_f32(row[e]));
+    if (l != -INFINITY) {
+      c = a.softmax ? exp(l - top) / z : 1.0 / (1.0 + exp(-l));
+      if (a.bias) c += (double)a.bias[e];
+    }
+  }
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(FULL, c, j);
+    const int oe = __shfl_sync(FULL, e, j);
+    rank += (o > c || (o == c && oe < e)) ? 1 : 0;
+  }
+  int mine = 0;
+  for (int j = 0; j < n; ++j) {
+    const int r = __shfl_sync(FULL, rank, j), oe = __shfl_sync(FULL, e, j);
+    if (r == lane) mine = oe;
+  }
+  return mine;
+}
+
 template <int PER, typename Tin>
 __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(const Args a) {
   extern __shared__ double smem[];   // [WARPS][E]
@@ -444,17 +507,9 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
     if (left == floor_key) left = 0u;
   }
   floor_key = max(floor_key, 1u);
-  int found = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const unsigned who = __ballot_sync(FULL, key[i] >= floor_key);
-    if (key[i] >= floor_key) {
-      const int at = found + __popc(who & ((1u << lane) - 1u));
-      if (at < 32) cand[warp][at] = make_uint2(key[i], (uint32_t)(e0 + i));
-    }
-    found += __popc(who);
-  }
-  if (found <= 32 && rounds <= 32) {
+  const int found = gather<PER>(key, floor_key, e0, lane, cand[warp]);
+  const bool ranked = found <= 32 && rounds <= 32;
+  if (ranked) {
     __syncwarp();
     const uint2 me = lane < found ? cand[warp][lane] : make_uint2(0u, 0u);
     int rank = 0;
@@ -509,8 +564,20 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
     if (lane == 31) after = next_key;
     const bool near = lane < k && after != 0u && !same && mine != -INFINITY &&
                       mine - of_key(after) <= tol_s + 0x1p-22f * fabsf(mine);
-    again = again || __any_sync(FULL, near);
-    if (again) my_e = choose_f64<PER>(row, a, smem + (size_t)warp * E, lane);
+    const bool unsure = __any_sync(FULL, near);
+    if (again || (unsure && !ranked)) {
+      my_e = choose_f64<PER>(row, a, smem + (size_t)warp * E, lane);
+    } else if (unsure) {
+      // the groups are certain: whatever may be among the k best is within the
+      // errors of the k-th
+      const float last = of_key(__shfl_sync(FULL, my_key, k - 1));
+      const float floor_c = last - (tol_s + 0x1p-22f * fabsf(last));
+      __syncwarp();
+      const int some = gather<PER>(key, max(key_of(floor_c), 1u), e0, lane, cand[warp]);
+      __syncwarp();
+      my_e = some <= 32 ? order_f64<PER>(row, a, cand[warp], some, lane)
+                        : choose_f64<PER>(row, a, smem + (size_t)warp * E, lane);
+    }
   }
   const float lj = lane < k ? logit_of(my_e) : -INFINITY;
   float wj;
