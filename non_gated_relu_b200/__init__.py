@@ -411,8 +411,10 @@ def _args(*specs):
     """Check device tensors, each (name, tensor, types, shape); returns their pointers.
     Types, shapes and layout of all come before the device of any."""
     ty = _types()
-    for name, t, dtypes, shape in specs:
-        if not isinstance(t, ty.Tensor):
+    Tensor, dev, off, out = ty.Tensor, None, None, []
+    for spec in specs:
+        name, t, dtypes, shape = spec
+        if not isinstance(t, Tensor):
             raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
         if t.dtype not in dtypes:
             raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
@@ -420,12 +422,17 @@ def _args(*specs):
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: tensors passed to libnhmoe must be contiguous")
-    out = [spec[1].data_ptr() or None for spec in specs]
-    if any(out):
-        dev = ty.current_device()
-        for (name, t, _, _), ptr in zip(specs, out):
-            if ptr and t.get_device() != dev:
-                raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+        ptr = t.data_ptr()
+        out.append(ptr or None)
+        if ptr and off is None:
+            if dev is None:
+                dev = t.get_device()
+                if dev < 0 or dev != ty.current_device():
+                    off = spec
+            elif t.get_device() != dev:
+                off = spec
+    if off is not None:
+        raise ValueError(f"{off[0]}: on {off[1].device}, not on the current CUDA device")
     return out
 
 
@@ -466,7 +473,7 @@ def gate(cfg: GateConfig, logits, bias, topk_idx, topk_w, stream=None):
     if bias is not None:
         specs.append(("bias", bias, ty.f32, (E,)))
     ptrs = _args(*specs)
-    _check(load().nh_moe_gate(ctypes.byref(cfg), T, ptrs[0], ptrs[3] if bias is not None else None,
+    _check((_lib or load()).nh_moe_gate(ctypes.byref(cfg), T, ptrs[0], ptrs[3] if bias is not None else None,
                               ptrs[1], ptrs[2], _stream(stream)))
 
 
@@ -478,7 +485,7 @@ def gate_backward(cfg: GateConfig, logits, topk_idx, d_topk_w, d_logits, stream=
     lt = ty.bf16 if cfg.dtype == NH_BF16 else ty.f32
     ptrs = _args(("logits", logits, lt, (T, E)), ("topk_idx", topk_idx, ty.i32, (T, k)),
                  ("d_topk_w", d_topk_w, ty.f32, (T, k)), ("d_logits", d_logits, lt, (T, E)))
-    _check(load().nh_moe_gate_backward(ctypes.byref(cfg), T, *ptrs, _stream(stream)))
+    _check((_lib or load()).nh_moe_gate_backward(ctypes.byref(cfg), T, *ptrs, _stream(stream)))
 
 
 def route_scored(cfg, scoring_func, x, w_router, bias, topk_idx, topk_w, ws, stream=None):
@@ -527,7 +534,7 @@ def fp8_quantize(x, codes, scales, stream=None):
     T, K = x.shape
     px, pc, ps = _args(("x", x, ty.act, (T, K)), ("codes", codes, ty.f8, (T, K)),
                        ("scales", scales, ty.f32, (T, -(-K // 128))))
-    _check(load().nh_fp8_quantize(T, K, px, _dt(x), pc, ps, _stream(stream)))
+    _check((_lib or load()).nh_fp8_quantize(T, K, px, _dt(x), pc, ps, _stream(stream)))
 
 
 def fp8_quantize_weight(w, codes=None, scales=None, stream=None):
@@ -545,13 +552,13 @@ def fp8_quantize_weight(w, codes=None, scales=None, stream=None):
         scales = torch.empty(blocks, dtype=torch.float32, device=w.device)
     pw, pc, ps = _args(("w", w, ty.act, (n, rows, cols)), ("codes", codes, ty.f8, (n, rows, cols)),
                        ("scales", scales, ty.f32, blocks))
-    _check(load().nh_fp8_quantize_weight(n, rows, cols, pw, _dt(w), pc, ps, _stream(stream)))
+    _check((_lib or load()).nh_fp8_quantize_weight(n, rows, cols, pw, _dt(w), pc, ps, _stream(stream)))
     return codes, scales
 
 
 def fp8_linear_workspace_size(T: int, N: int, K: int) -> int:
     n = ctypes.c_size_t()
-    _check(load().nh_fp8_linear_workspace_size(T, N, K, ctypes.byref(n)))
+    _check((_lib or load()).nh_fp8_linear_workspace_size(T, N, K, ctypes.byref(n)))
     return n.value
 
 
@@ -564,7 +571,7 @@ def fp8_linear(x, w: Fp8Weight, y, ws, stream=None):
     N = y.shape[1]
     ref = _fp8("w", w, (1, N, K))
     px, py = _args(("x", x, ty.act, (T, K)), ("y", y, ty.act, (T, N)))
-    _check(load().nh_fp8_linear(T, N, K, px, _dt(x), ref, py, _dt(y), *_ws_arg("ws", ws),
+    _check((_lib or load()).nh_fp8_linear(T, N, K, px, _dt(x), ref, py, _dt(y), *_ws_arg("ws", ws),
                                 _stream(stream)))
 
 
@@ -584,7 +591,7 @@ def forward_fp8(cfg, x, w_up: Fp8Weight, w_down: Fp8Weight, ws, y_acc, stream=No
     c = config_from(cfg)
     T, px, py = _f8_args(c, x, y_acc)
     E, H, I = c.n_routed_experts, c.hidden_size, c.moe_intermediate_size
-    _check(load().nh_moe_forward_fp8(ctypes.byref(c), T, px, _fp8("w_up", w_up, (E, I, H)),
+    _check((_lib or load()).nh_moe_forward_fp8(ctypes.byref(c), T, px, _fp8("w_up", w_up, (E, I, H)),
                                      _fp8("w_down", w_down, (E, H, I)), *_ws_arg("ws", ws), py,
                                      _stream(stream)))
 

@@ -441,6 +441,7 @@ static uint64_t timeout_ns() {
 // block scheduler then starts pending CTAs of the routed path (a high
 // priority stream) before those of the concurrent shared expert.
 static int stream_priority(cudaStream_t st) {
+  if (!st) return 0;   // the default stream has the default priority
   int p = 0;
   if (cudaStreamGetPriority(st, &p) != cudaSuccess) {
     cudaGetLastError();
