@@ -12,8 +12,12 @@
 // (each stages 128 rows of both operands).  Per K block of a tile the MMAs take
 // 512 cycles and the multiply-adds 256 of each SM's float32 units; what sets the
 // rate is how long an accumulator is away from the tensor cores: a drain warp
-// takes its 128 columns in two loads of 64 and hands the accumulator back before
-// it adds the second.  A thread owns one row and 128 features, which makes the
+// takes its 128 columns in four loads, each in flight while the one before is
+// added, and hands the accumulator back before it adds the last.  Measured: a K
+// block every 700 to 800 cycles and 2000 to 3500 for the end of a tile; 16384 x
+// 3712 x 2688 in 163 us (2.0 PFLOP/s, at the power limit), the experts' two
+// products of 16384 tokens (128 experts of 2688 x 1856, 6 taken) in 663 and 785.
+// A thread owns one row and 128 features, which makes the
 // scale one number per thread and block, and leaves the maximum of a (row, 128
 // features) block of the output inside one thread, where the next projection's
 // quantization needs it.
@@ -24,7 +28,7 @@
 // the other eight, whose sums would spill in an even split.  Producer and
 // issuer run their loops as whole warps and elect a lane for the instruction
 // itself: descriptors and addresses then stay in uniform registers (one lane in
-// a branch of its own needed 700 cycles to issue a K block).  Tiles are dealt
+// a branch of its own needed 700 cycles to issue a K block, this way it takes 140).  Tiles are dealt
 // out in turn (tile i to pair i mod pairs): they all take the same time.  Both
 // CTAs' copies complete on the leader's stage barrier, MMA completion is
 // committed to both CTAs, the peer's drains arrive on the leader's barriers.

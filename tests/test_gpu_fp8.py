@@ -518,6 +518,51 @@ def test_experts_repeat_and_graph():
         assert ((y.float() - want).abs() <= 2.0 ** -7 * want.abs() + 1e-5 * want.abs().amax()).all()
 
 
+def test_products_on_several_streams_at_once():
+    """A small-batch and a large-batch experts call, a linear call and a GEMV side by
+    side: kernels that share SMs and tensor memory, each with its own workspace."""
+    gen = generator(41)
+    small, large = config(8, hidden_size=704, moe_intermediate_size=576), config(6000, n_routed_experts=8)
+    jobs = []
+    for cfg in (small, large):
+        c = nh.config_from(cfg)
+        up, down = experts_case(cfg, gen)
+        fu, fd = nh.fp8_weight(*up), nh.fp8_weight(*down)
+        idx, w = routing(cfg.T, cfg.E, cfg.k, gen)
+        x = torch.randn((cfg.T, cfg.H), generator=gen, device=DEV).to(B16)
+        ws = torch.zeros(nh.workspace_size(c, cfg.T), dtype=torch.uint8, device=DEV)
+        y = torch.zeros((cfg.T, cfg.H), device=DEV)
+
+        def experts(stream=None, c=c, T=cfg.T, fu=fu, fd=fd, idx=idx, w=w, x=x, ws=ws, y=y):
+            nh.zero_acc(c, T, y, stream=stream)
+            nh.permute(c, x, idx, w, ws, stream=stream)
+            nh.forward_fp8(c, x, fu, fd, ws, y, stream=stream)
+        jobs.append((experts, y, ws, False))
+    for T in (4, 900):
+        wt = nh.fp8_weight(*ref.make_weight(gen, 1, 1856, 2688))
+        x = torch.randn((T, 2688), generator=gen, device=DEV).to(B16)
+        y = torch.zeros((T, 1856), dtype=B16, device=DEV)
+        ws = torch.zeros(nh.fp8_linear_workspace_size(T, 1856, 2688), dtype=torch.uint8, device=DEV)
+        jobs.append((lambda stream=None, x=x, wt=wt, y=y, ws=ws: nh.fp8_linear(x, wt, y, ws, stream=stream),
+                     y, ws, True))
+    want = []
+    for job, y, _, _ in jobs:
+        job()
+        torch.cuda.synchronize()
+        want.append(y.clone())
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(12):
+        for (job, *_), st in zip(jobs, streams):
+            job(st)
+    torch.cuda.synchronize()
+    for (_, y, ws, same_bits), ref_y in zip(jobs, want):
+        assert nh.check_device(ws) == 0
+        if same_bits:
+            assert torch.equal(y, ref_y)
+        else:      # up to the order of the float32 adds of a token's k rows
+            assert ((y - ref_y).abs() <= 2.0 ** -20 * (ref_y.abs().amax() + ref_y.abs())).all()
+
+
 # -- the block ---------------------------------------------------------------------------
 def block_and_parts(cfg, seed=0, bias=False):
     gen = generator(seed)
