@@ -72,6 +72,12 @@ def _to_device(a, dtype: torch.dtype, device) -> torch.Tensor:
     return t.to(device).contiguous()
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t, contiguous and on a 16-byte boundary (a slice of a tensor may be on neither)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 @dataclass
 class Buffers:
     T: int
@@ -146,7 +152,7 @@ class NemotronHMoE:
                 raise ValueError("config has FP8 weights: pass fp8={...}")
             # fp8_weight keeps the device tensors
             with torch.cuda.device(self.device):
-                self.f8 = {name: fp8_weight(*(torch.as_tensor(a).to(self.device).contiguous()
+                self.f8 = {name: fp8_weight(*(_aligned(torch.as_tensor(a).to(self.device))
                                               for a in pair)) for name, pair in fp8.items()}
             self._check_fp8()
             self.w_up = self.w_down = self.w_shared_up = self.w_shared_down = None

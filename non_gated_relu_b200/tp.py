@@ -21,6 +21,10 @@ block when 64 * world does not divide I (Nemotron-H's I = 1856 is 29
 blocks).  Each rank adds its own contributions into its float32
 accumulator y_acc without rounding; the all-reduce sums those in float32 and
 nh_moe_finalize rounds the sum once, as the unsharded block does.
+
+FP8 weights are cut in blocks of 128 features, their scale blocks (the last one may
+be shorter), so a rank quantizes its hidden features in the blocks of the unsharded
+block and gets the same codes.
 """
 from __future__ import annotations
 
@@ -48,16 +52,35 @@ def shard_range(n: int, world: int, rank: int, block: int = BLOCK) -> Tuple[int,
     return (rank * nb // world) * block, ((rank + 1) * nb // world) * block
 
 
+FP8_BLOCK = 128
+
+
+def shard_range_fp8(n: int, world: int, rank: int) -> Tuple[int, int]:
+    """[start, stop) of rank's share of n features in blocks of 128, of which the last
+    may be shorter."""
+    if world < 1 or not 0 <= rank < world:
+        raise ValueError(f"rank {rank} of world {world}")
+    nb = -(-n // FP8_BLOCK)
+    if nb < world:
+        raise ValueError(f"{n} features ({nb} blocks of {FP8_BLOCK}) cannot feed {world} ranks")
+    return (rank * nb // world) * FP8_BLOCK, min(n, ((rank + 1) * nb // world) * FP8_BLOCK)
+
+
+def _range_of(cfg):
+    return shard_range_fp8 if config_from(cfg).weight_format == NH_WEIGHTS_FP8 else shard_range
+
+
 def _replace(cfg, **kw):
     return cfg.replace(**kw) if hasattr(cfg, "replace") else dataclasses.replace(cfg, **kw)
 
 
 def shard_config(cfg, world: int, rank: int):
     """The config a rank runs: its shares of I and S (S stays 0 without a shared expert)."""
-    i0, i1 = shard_range(cfg.moe_intermediate_size, world, rank)
+    cut = _range_of(cfg)
+    i0, i1 = cut(cfg.moe_intermediate_size, world, rank)
     kw = dict(moe_intermediate_size=i1 - i0)
     if cfg.n_shared_experts:
-        s0, s1 = shard_range(cfg.moe_shared_expert_intermediate_size, world, rank)
+        s0, s1 = cut(cfg.moe_shared_expert_intermediate_size, world, rank)
         kw["moe_shared_expert_intermediate_size"] = s1 - s0
     return _replace(cfg, **kw)
 
@@ -117,6 +140,27 @@ def shard_nvfp4(cfg, world: int, rank: int, q: dict) -> dict:
     return out
 
 
+def _slice_fp8(q, start: int, stop: int, over_inputs: bool):
+    """Features [start, stop) of a stacked FP8 weight (codes, scales); start on a scale
+    block."""
+    codes, scales = q
+    b = slice(start // FP8_BLOCK, -(-stop // FP8_BLOCK))
+    if over_inputs:
+        return _contig(codes[:, :, start:stop]), _contig(scales[:, :, b])
+    return _contig(codes[:, start:stop, :]), _contig(scales[:, b, :])
+
+
+def shard_fp8(cfg, world: int, rank: int, q: dict) -> dict:
+    """Rank's slices of FP8 weights {"up", "down", "shared_up", "shared_down"}."""
+    i0, i1 = shard_range_fp8(cfg.moe_intermediate_size, world, rank)
+    out = {"up": _slice_fp8(q["up"], i0, i1, False), "down": _slice_fp8(q["down"], i0, i1, True)}
+    if cfg.n_shared_experts and "shared_up" in q:
+        s0, s1 = shard_range_fp8(cfg.moe_shared_expert_intermediate_size, world, rank)
+        out["shared_up"] = _slice_fp8(q["shared_up"], s0, s1, False)
+        out["shared_down"] = _slice_fp8(q["shared_down"], s0, s1, True)
+    return out
+
+
 def all_reduce_sum(y: torch.Tensor, group=None) -> torch.Tensor:
     """Sum y over the ranks of `group` in place (one collective; a no-op for
     one rank or without an initialised process group)."""
@@ -137,7 +181,7 @@ class TPNemotronHMoE:
 
     def __init__(self, cfg, w_router, w_up=None, w_down=None, w_shared_up=None,
                  w_shared_down=None, bias=None, nvfp4=None, group=None,
-                 world: Optional[int] = None, rank: Optional[int] = None, device=None):
+                 world: Optional[int] = None, rank: Optional[int] = None, device=None, fp8=None):
         import torch.distributed as dist
         dist_on = dist.is_available() and dist.is_initialized()
         self.world = world if world is not None else (dist.get_world_size(group) if dist_on else 1)
@@ -146,19 +190,21 @@ class TPNemotronHMoE:
         self.cfg = cfg
         if getattr(cfg, "latent_size", 0):
             raise NotImplementedError("tensor parallelism of a latent block is not built")
-        if config_from(cfg).weight_format == NH_WEIGHTS_FP8:
-            # shards are cut in blocks of 64 features, scale blocks are 128 wide
-            raise NotImplementedError("tensor parallelism of FP8 expert weights is not built")
         self.cfg_rank = shard_config(cfg, self.world, self.rank)
-        q = None
+        q = q8 = None
         if config_from(cfg).weight_format == NH_WEIGHTS_NVFP4:
             q = shard_nvfp4(cfg, self.world, self.rank, nvfp4)
+            up = down = su = sd = None
+        elif config_from(cfg).weight_format == NH_WEIGHTS_FP8:
+            if fp8 is None:
+                raise ValueError("config has FP8 weights: pass fp8={...}")
+            q8 = shard_fp8(cfg, self.world, self.rank, fp8)
             up = down = su = sd = None
         else:
             up, down, su, sd = shard_weights(cfg, self.world, self.rank, w_up, w_down,
                                              w_shared_up, w_shared_down)
         self.block = NemotronHMoE(self.cfg_rank, w_router, up, down, su, sd, bias=bias,
-                                  device=device, nvfp4=q)
+                                  device=device, nvfp4=q, fp8=q8)
         self.c_full = config_from(cfg)
         self._y = {}
 

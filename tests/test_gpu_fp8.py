@@ -630,6 +630,28 @@ def _near(y, want):
     return True
 
 
+@pytest.mark.parametrize("T", [8, 40, 700])
+@pytest.mark.parametrize("world", [2, 3])
+def test_tensor_parallel_ranks_sum_to_the_block(T, world):
+    """Rank by rank on one GPU: hidden codes are those of the whole block (the cuts lie on
+    scale blocks), so the float32 partials add up to its accumulator but for the order of
+    the sums: E k K blocks' roundings of the terms' magnitudes."""
+    from non_gated_relu_b200 import tp
+    cfg = config(T, moe_intermediate_size=448, moe_shared_expert_intermediate_size=576)
+    blk, f8, wr, b, _, gen = block_and_parts(cfg, T, bias=True)
+    x = torch.randn((T, cfg.H), generator=gen, device=DEV).to(B16)
+    whole = blk.forward(x, partial=True).clone()
+    parts = []
+    for r in range(world):
+        rank = tp.TPNemotronHMoE(cfg, wr, fp8=f8, bias=b, world=world, rank=r)
+        parts.append(rank.partial(x).clone())
+        assert rank.block.check(T) == 0
+    total = sum(parts)
+    size = sum(p.abs() for p in parts) + whole.abs().amax()
+    assert ((total - whole).abs() <= 2.0 ** -18 * size).all()
+    assert _near(rank.output(total), whole.double())
+
+
 def test_block_needs_its_weights():
     cfg = config(8)
     blk, f8, wr, *_ = block_and_parts(cfg)

@@ -198,11 +198,41 @@ def test_fp8_workspace_holds_codes_and_scales(T):
     assert L.total_bytes == nh.workspace_size(cfg, T)
 
 
-def test_tp_refuses_fp8():
+@pytest.mark.parametrize("n,world", [(1856, 2), (1856, 3), (3712, 4), (192, 2), (128, 1)])
+def test_fp8_shards_are_whole_scale_blocks(n, world):
     from non_gated_relu_b200 import tp
-    cfg = synth.CONFIGS["decode_bf16_t8"].replace(weight_format="fp8")
-    with pytest.raises(NotImplementedError):
-        tp.TPNemotronHMoE(cfg, None, world=2, rank=0)
+    cuts = [tp.shard_range_fp8(n, world, r) for r in range(world)]
+    assert cuts[0][0] == 0 and cuts[-1][1] == n
+    assert all(a[1] == b[0] for a, b in zip(cuts, cuts[1:]))
+    assert all(s % 128 == 0 and e > s and (e - s) % 64 == 0 for s, e in cuts)
+    with pytest.raises(ValueError):
+        tp.shard_range_fp8(n, -(-n // 128) + 1, 0)
+    with pytest.raises(ValueError):
+        tp.shard_range_fp8(n, world, world)
+
+
+def test_fp8_shards_hold_the_weights_values():
+    torch = pytest.importorskip("torch")
+    import fp8_util as ref
+    from non_gated_relu_b200 import tp
+    gen = torch.Generator().manual_seed(0)
+    cfg = synth.CONFIGS["decode_bf16_t8"].replace(
+        weight_format="fp8", hidden_size=256, n_routed_experts=8, n_group=1, topk_group=1,
+        moe_intermediate_size=320, moe_shared_expert_intermediate_size=448)
+    q = {"up": ref.make_weight(gen, 8, 320, 256), "down": ref.make_weight(gen, 8, 256, 320),
+         "shared_up": ref.make_weight(gen, 1, 448, 256), "shared_down": ref.make_weight(gen, 1, 256, 448)}
+    for world in (1, 2, 3):
+        parts = {k: [] for k in q}
+        for r in range(world):
+            c = tp.shard_config(cfg, world, r)
+            sh = tp.shard_fp8(cfg, world, r, q)
+            assert sh["up"][0].shape == (8, c.moe_intermediate_size, 256)
+            assert sh["shared_down"][0].shape[2] == c.moe_shared_expert_intermediate_size
+            for k in q:
+                parts[k].append(ref.weight_values(*sh[k]))
+        for k in q:
+            got = torch.cat(parts[k], dim=2 if k.endswith("down") else 1)
+            assert torch.equal(got, ref.weight_values(*q[k]))
 
 
 def test_python_argument_checks():
