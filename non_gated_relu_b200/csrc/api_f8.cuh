@@ -237,6 +237,7 @@ static nh_status f8_shared(const nh_moe_config* cfg, int64_t T, const void* x,
   down.x = h.codes;
   down.xs = h.scales;
   down.x_rows = T;
+  down.early_w = true;   // the launch before is this call's up projection
   return run_f8(down, dev, st);
 }
 

@@ -1,5 +1,6 @@
 // gemm_f8s.cuh -- block-scaled FP8 product with the weights on the MMA M side:
-// the routed experts' form for batches that leave an expert few rows.
+// the routed experts' form for batches that leave an expert few rows, and the
+// dense form of as many rows as give each SM one tile of 64.
 //
 //   acc[n, r] = sum_b sw[n / 128, b] sx[r, b] (wq[n] . xq[r] over K block b of 128)
 //
@@ -45,13 +46,17 @@ constexpr int NBUF = 4;            // accumulators
 enum Out : int {
   OUT_RELU2_F8 = 0,  // out E4M3 [rows, N] of relu(acc)^2, scales [rows, ceil(N / 128)]
   OUT_COMBINE = 1,   // out f32: out[dst_row[r]] += perm_w[r] * acc, atomic adds
+  OUT_BF16 = 2,      // out bf16 [rows, N] = acc
+  OUT_F32 = 3,       // out f32 [rows, N] = acc
+  OUT_ADD_F32 = 4,   // out f32 [rows, N] += acc, atomic adds
 };
 
 struct Args {
   const float* xs;         // [rows, KB]
   const float* ws;         // [E, ceil(N / 128), KB]
-  const int4* tiles;       // (expert, first row, rows <= NT, -)
+  const int4* tiles;       // (expert, first row, rows <= NT, -) or null: dense rows
   const int32_t* num_tiles;
+  int dense_rows;
   int N, K, KB;
   void* out;
   float* out_scales;       // OUT_RELU2_F8
@@ -104,6 +109,12 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&v)[NC]) 
 #pragma unroll
     for (int c = 0; c < NC; c += 8) tmem_ld8(taddr + c, v + c);
   }
+}
+
+template <int NT>
+__device__ __forceinline__ int4 entry(const Args& g, int m) {
+  if (g.tiles) return g.tiles[m];
+  return make_int4(0, m * NT, min(NT, g.dense_rows - m * NT), 0);
 }
 
 template <int NT, int STAGES, int CTAS, int OUT>
@@ -163,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   const WaitCtl wc{abort_flag, g.status, g.timeout_ns};
 
   const int n_blocks = (g.N + M - 1) / M;
-  const int num_m = *g.num_tiles;
+  const int num_m = g.tiles ? *g.num_tiles : (g.dense_rows + NT - 1) / NT;
   const int step_m = gridDim.x / n_blocks, step_nb = gridDim.x - step_m * n_blocks;
   f8g::TileWalk t{(int)blockIdx.x / n_blocks, (int)blockIdx.x % n_blocks};
   const int nk = g.KB;
@@ -182,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
         if (f8g::elect_one()) {
           mbar_arrive_expect_tx(full_bar(ahead), S::STAGE_BYTES);
           tma_load_3d(base + ahead * S::STAGE_BYTES, &map_w, full_bar(ahead), kb * BK, e.nb * M,
-                      g.tiles[e.m].x);
+                      entry<NT>(g, e.m).x);
         }
         if (++kb == nk) {
           kb = 0;
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       for (int s = 0; s < ahead; ++s) {
         if (f8g::elect_one())
           tma_load_2d(base + s * S::STAGE_BYTES + S::W_BYTES, &map_x, full_bar(s), kb * BK,
-                      g.tiles[e.m].y);
+                      entry<NT>(g, e.m).y);
         if (++kb == nk) {
           kb = 0;
           e.next(n_blocks, step_m, step_nb);
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
     }
     long skip = issued;        // stages of the loop below that are under way already
     for (; ok && t.m < num_m; t.next(n_blocks, step_m, step_nb)) {
-      const int4 ent = g.tiles[t.m];
+      const int4 ent = entry<NT>(g, t.m);
       for (int kb = 0; kb < nk; ++kb) {
         if (skip > 0) {
           --skip;
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
     uint32_t use = 0, tiles_done = 0;
     bool ok = true;
     for (; ok && t.m < num_m; t.next(n_blocks, step_m, step_nb)) {
-      const int4 ent = g.tiles[t.m];
+      const int4 ent = entry<NT>(g, t.m);
       const float* ws = g.ws + ((size_t)ent.x * n_blocks + t.nb) * nk;
       const float* xs[CL];
       float sx[CL], sw = __ldg(ws);
@@ -342,6 +353,18 @@ __global__ void __launch_bounds__(THREADS, CTAS)
           if (c < cols && f < g.N)
             red_add_f32(static_cast<float*>(g.out) + (size_t)row * g.N + f, w * acc[c]);
         }
+      } else if constexpr (OUT != OUT_RELU2_F8) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (c < cols && f < g.N) {
+            const size_t at = (size_t)(ent.y + half * NC + c) * g.N + f;
+            if constexpr (OUT == OUT_BF16)
+              static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(acc[c]);
+            else if constexpr (OUT == OUT_F32)
+              static_cast<float*>(g.out)[at] = acc[c];
+            else
+              red_add_f32(static_cast<float*>(g.out) + at, acc[c]);
+          }
       } else {
         uint32_t top[CL];
 #pragma unroll

@@ -84,6 +84,7 @@ constexpr int ROUTE_PERMUTE_SMEM_MAX = (16 * 256 + 256 + 3 * 32 * 32) * 4;
 
 constexpr int F8_GEMV_ROWS = 32;   // rows up to which dense FP8 products run as GEMVs
 constexpr int F8_RAW_ROWS = 8;     // and up to which those quantize their rows themselves
+constexpr int F8_DENSE_NT = 64;    // rows of a dense tile with the weights on the M side
 
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -348,6 +349,14 @@ static nh_status f8_swap_attrs() {
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_COMBINE>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if constexpr (NT == F8_DENSE_NT) {
+    NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_BF16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_F32>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_ADD_F32>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  }
   return NH_OK;
 }
 

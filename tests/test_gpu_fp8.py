@@ -148,6 +148,21 @@ def test_linear(T, N, K):
     assert rel <= 2e-5
 
 
+@pytest.mark.parametrize("T,N,K", [(9537, 16, 16), (9601, 64, 128), (3300, 272, 144),
+                                   (2400, 400, 1136), (700, 1856, 144), (449, 3712, 2688),
+                                   (320, 3712, 2688), (640, 1856, 2688), (321, 3712, 2688)])
+def test_linear_many_rows(T, N, K):
+    """On both sides of one tile of 128 features x 64 rows for each SM, where the form
+    changes; last tiles of 1 to 63 rows and of 16 features."""
+    gen = generator(T * 31 + N)
+    codes, scales = ref.make_weight(gen, 1, N, K)
+    w = nh.fp8_weight(codes, scales)
+    wv = ref.weight_values(codes[0], scales[0])
+    x = torch.randn((T, K), generator=gen, device=DEV)
+    check_product(linear(x.to(B16), w, N), ref.rows_values(x.to(B16)), wv, K)
+    assert check_product(linear(x, w, N, F32), ref.rows_values(x), wv, K) <= 2e-5
+
+
 def test_linear_many_tiles():
     """More tiles than CTA pairs, a last tile of 32 features, and rows of every size."""
     gen = generator(4)
@@ -405,6 +420,44 @@ def test_experts(T, kw):
     b = check_experts(cfg, x, idx, w, up, down, split=True)
     # the same up to the order of the float32 adds of a token's k rows
     assert ((a - b).abs() <= 2.0 ** -22 * cfg.k * (a.abs().amax() + b.abs())).all()
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 32, 33, 64, 65, 300, 321, 1500])
+@pytest.mark.parametrize("H,S", [(256, 320), (64, 64), (2688, 3712)])
+def test_shared(T, H, S):
+    """Each hidden value lies between the codes of its exact value's two ends, and y between
+    the products of those ends, but for the rounding of S terms and the add."""
+    gen = generator(T + S)
+    cfg = config(T, hidden_size=H, moe_shared_expert_intermediate_size=S)
+    c = nh.config_from(cfg)
+    su, sd = ref.make_weight(gen, 1, S, H), ref.make_weight(gen, 1, H, S)
+    x = torch.randn((T, H), generator=gen, device=DEV).to(B16)
+    ws = torch.zeros(nh.shared_workspace_size(c, T), dtype=torch.uint8, device=DEV)
+    y = torch.full((T + 1, H), float("nan"), device=DEV)
+    nh.shared_store_fp8(c, x, nh.fp8_weight(*su), nh.fp8_weight(*sd), y[:T], ws)
+    y0 = torch.randn((T + 1, H), generator=gen, device=DEV)
+    y1 = y0.clone()
+    nh.shared_fp8(c, x, nh.fp8_weight(*su), nh.fp8_weight(*sd), y1[:T], ws)
+    assert nh.check_device(ws) == 0
+    assert y[T].isnan().all() and torch.equal(y0[T], y1[T])
+    uv, dv = ref.weight_values(su[0][0], su[1][0]), ref.weight_values(sd[0][0], sd[1][0])
+    xv = ref.rows_values(x)
+    pre, err = xv @ uv.t(), (xv.abs() @ uv.abs().t()) * gamma(H)
+    ends = (torch.relu(pre - err) ** 2 * (1 - 2.0 ** -22), torch.relu(pre + err) ** 2 * (1 + 2.0 ** -22))
+    kb = -(-S // 128)
+    pad = torch.nn.functional.pad
+    sp = [ref.spread(ref.block_scale(pad(v, (0, kb * 128 - S)).view(T, kb, 128).amax(dim=2)), S)
+          for v in ends]
+    code = lambda v, s: ref.nearest_e4m3((v / s).clamp(max=448)) * s  # noqa: E731
+    lo = torch.minimum(code(ends[0], sp[0]), code(ends[0], sp[1]))
+    hi = torch.maximum(code(ends[1], sp[0]), code(ends[1], sp[1]))
+    pos, neg = dv.clamp(min=0).t(), dv.clamp(max=0).t()
+    tol = (hi @ dv.abs().t()) * gamma(S) + 1e-30
+    low, high = lo @ pos + hi @ neg - tol, hi @ pos + lo @ neg + tol
+    assert ((y[:T] >= low) & (y[:T] <= high)).all()
+    add = y0[:T].double()
+    edge = 2.0 ** -24 * (add.abs() + torch.maximum(low.abs(), high.abs()))
+    assert ((y1[:T] >= add + low - edge) & (y1[:T] <= add + high + edge)).all()
 
 
 def test_experts_with_weights_past_32_bits():
