@@ -502,7 +502,7 @@ nh_status nh_fp8_quantize_weight(int64_t n_mat, int64_t rows, int64_t cols, cons
  *   aligned, holding a status word (cleared by the caller, once:
  *   nh_moe_reset_status; this call records device faults in it) and the
  *   quantized x.  Calls that may overlap need their own ws.
- * Up to 32 tokens run as a GEMV over the weights, more on 256 x 256 tiles; for
+ * Up to 32 tokens run as a GEMV over the weights, more on tensor-core tiles; for
  * given inputs a result does not depend on scheduling.
  */
 nh_status nh_fp8_linear_workspace_size(int64_t T, int64_t N, int64_t K, size_t *bytes);

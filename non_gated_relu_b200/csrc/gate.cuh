@@ -240,8 +240,8 @@ __device__ __forceinline__ uint64_t keep_groups(const V* c, int G, int g, int tg
       if (a) last = va;
       if (b) next = vb;
     }
-    // two group values that are both -inf tie exactly
-    *close = (float)(last - next) <= tol_s + 0x1p-22f * fabsf((float)last);
+    // two group values that are both -inf tie exactly; a sum of two may be +inf
+    *close = last != -INFINITY && !((float)(last - next) > tol_s + 0x1p-22f * fabsf((float)last));
   }
   return keep;
 }
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
       const unsigned lb = __ballot_sync(FULL, in && rank == a.tg);
       const float last = __shfl_sync(FULL, gs, __ffs(la) - 1);
       const float next = __shfl_sync(FULL, gs, __ffs(lb) - 1);
-      close = last - next <= 2.f * tol_s + 0x1p-22f * fabsf(last);
+      close = last != -INFINITY && !(last - next > 2.f * tol_s + 0x1p-22f * fabsf(last));
       if (rank >= a.tg) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) key[i] = 0u;
@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
       __syncwarp();
       const int some = gather<PER>(key, max(key_of(floor_c), 1u), e0, lane, cand[warp]);
       __syncwarp();
-      my_e = some <= 32 ? order_f64<PER>(row, a, cand[warp], some, lane)
-                        : choose_f64<PER>(row, a, smem + (size_t)warp * E, lane);
+      my_e = some >= k && some <= 32 ? order_f64<PER>(row, a, cand[warp], some, lane)
+                                     : choose_f64<PER>(row, a, smem + (size_t)warp * E, lane);
     }
   }
   const float lj = lane < k ? logit_of(my_e) : -INFINITY;

@@ -105,6 +105,30 @@ def test_neighbours_closer_than_float32_scores(softmax):
 
 
 @pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("top2", [False, True])
+def test_biases_near_the_ends_of_float32(softmax, top2):
+    """Group values that overflow float32 are told apart all the same; a bias of +inf (not
+    of the documented values) still gives k different experts, those first."""
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    inf, big = math.inf, 3.2e38
+    for E, G, tg, k in ((64, 8, 3, 6), (100, 10, 4, 8), (128, 1, 1, 6)):
+        x = torch.randn((50, E), generator=gen, device=DEV)
+        x[:5, ::3] = -inf
+        x[5, E // 2:] = -inf
+        for _ in range(4):
+            at = torch.randint(0, 5, (E,), generator=gen, device=DEV)
+            step = 1 + torch.rand(E, generator=gen, device=DEV) * 2.0 ** -6
+            b = torch.tensor([big, -big, 2.9e38, 0.0, 1.0], device=DEV)[at] * step
+            check(x, b, G, tg, k, softmax, True, top2)
+        b = torch.zeros(E, device=DEV)
+        b[3:3 + k] = inf
+        _, idx, w = run(x, b, 1, 1, k, softmax, True, False)
+        free = x[:, 3:3 + k].isfinite().all(dim=1)
+        assert (idx[free] == torch.arange(3, 3 + k, device=DEV)).all()
+        assert all(r.unique().numel() == k for r in idx) and w.isfinite().all()
+
+
+@pytest.mark.parametrize("softmax", [False, True])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("norm", [False, True])
 def test_masked_and_non_finite_rows(softmax, bias, norm):
