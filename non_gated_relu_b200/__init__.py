@@ -69,7 +69,7 @@ class NvFp4Weight(ctypes.Structure):
 
 class Fp8Weight(ctypes.Structure):
     """nh_fp8_weight: device pointers of one stacked FP8 tensor (and, on the Python
-    side, its shape and the tensors themselves)."""
+    side, its shape, device and the tensors themselves)."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
@@ -514,7 +514,7 @@ def fp8_weight(codes, scales) -> Fp8Weight:
     n, rows, cols = codes.shape
     w = Fp8Weight(*_args(("codes", codes, ty.f8, (n, rows, cols)),
                          ("scales", scales, ty.f32, (n, -(-rows // 128), -(-cols // 128)))))
-    w.shape, w.tensors = (n, rows, cols), (codes, scales)
+    w.shape, w.device, w.tensors = (n, rows, cols), codes.get_device(), (codes, scales)
     return w
 
 
@@ -524,6 +524,8 @@ def _fp8(name, w, shape):
     got = getattr(w, "shape", None)
     if got is not None and got != tuple(shape):
         raise ValueError(f"{name}: expected codes of shape {tuple(shape)}, got {got}")
+    if got is not None and w.device != _types().current_device():
+        raise ValueError(f"{name}: on cuda:{w.device}, not on the current CUDA device")
     return ctypes.byref(w)
 
 

@@ -257,3 +257,14 @@ def test_python_argument_checks():
     if not torch.cuda.is_available():
         with pytest.raises((ValueError, RuntimeError, AssertionError)):
             nh.gate(c, f, None, i, w)                          # host tensors
+
+
+def test_weights_of_another_device_are_refused(monkeypatch):
+    pytest.importorskip("torch")
+    w = nh.Fp8Weight(256, 256)
+    w.shape, w.device = (1, 64, 128), 1
+    monkeypatch.setattr(nh._types(), "current_device", lambda: 1)
+    nh._fp8("w", w, (1, 64, 128))
+    monkeypatch.setattr(nh._types(), "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="cuda:1"):
+        nh._fp8("w", w, (1, 64, 128))
