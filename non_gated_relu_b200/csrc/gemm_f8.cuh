@@ -13,8 +13,9 @@
 // 512 cycles and the multiply-adds 256 of each SM's float32 units; what sets the
 // rate is how long an accumulator is away from the tensor cores: a drain warp
 // takes its 128 columns in four loads, each in flight while the one before is
-// added, and hands the accumulator back before it adds the last.  Measured: a K
-// block every 700 to 800 cycles and 2000 to 3500 for the end of a tile; 16384 x
+// added, and hands the accumulator back before it adds the last.  They wait without
+// the sleep hint (a K block of a lone pair 461 -> 449 ns).  Measured: a K
+// block every 700 to 850 cycles and 2000 to 3500 for the end of a tile; 16384 x
 // 3712 x 2688 in 163 us (2.0 PFLOP/s, at the power limit), the experts' two
 // products of 16384 tokens (128 experts of 2688 x 1856, 6 taken) in 663 and 785.
 // A thread owns one row and 128 features, which makes the
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int kb = 0; kb < nk; ++kb, ++use) {
         const uint32_t a = use & 1u, from = tq + a * NT;
         // the warp leaves together, also where a wait runs out for some lanes
-        ok = __all_sync(0xffffffffu, mbar_wait(done_bar(stage), phase, wc, SITE_TC_EPILOGUE));
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(done_bar(stage), phase, wc, SITE_TC_EPILOGUE));
         if (!ok) break;
         if (++stage == STAGES) {
           stage = 0;

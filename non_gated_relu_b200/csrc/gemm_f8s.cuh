@@ -12,8 +12,8 @@
 // arrive, and the rate is that of memory as long as enough bytes are under way:
 // two CTAs per SM, each with about 100 KB of stages (one CTA of 192 KB, as 128
 // rows a tile would need, drew 3.7 TB/s where two draw 6).  Measured: 64 tokens,
-// 6 of 128 experts of 2688 x 1856 each, 116 experts hit: 93 and 96 us for the two
-// projections, 6.2 TB/s; 8 tokens (37 hit): 34 and 32 us, 5.6 TB/s.  As in
+// 6 of 128 experts of 2688 x 1856 each, 116 experts hit: 92 us for each of the two
+// projections, 6.3 TB/s; 8 tokens (37 hit): 33 and 32 us, 5.6 TB/s.  As in
 // the pair kernel each K block is its own accumulator, four in turn, drained
 // into registers times its scales by eight warps (warp w: weight rows of quarter
 // w mod 4, half of the columns); the weight scale is one number per block and the
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
         if (skip > 0) {
           --skip;
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, wc, SITE_TC_PRODUCER));
+          ok = __all_sync(0xffffffffu, mbar_wait_spin(empty_bar(stage), phase ^ 1u, wc, SITE_TC_PRODUCER));
           if (!ok) break;
           if (f8g::elect_one()) {
             const uint32_t sw = base + stage * S::STAGE_BYTES;
@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       for (int kb = 0; kb < nk; ++kb, ++use) {
         const uint32_t a = use % NBUF;
         ok = __all_sync(0xffffffffu,
-                        mbar_wait(full_bar(stage), phase, wc, SITE_TC_MMA) &&
-                            mbar_wait(tempty_bar(a), ((use / NBUF) & 1u) ^ 1u, wc, SITE_TC_MMA));
+                        mbar_wait_spin(full_bar(stage), phase, wc, SITE_TC_MMA) &&
+                            mbar_wait_spin(tempty_bar(a), ((use / NBUF) & 1u) ^ 1u, wc, SITE_TC_MMA));
         if (!ok) break;
         tc_fence_after();
         const uint64_t dw = sdesc0 + (uint64_t)(stage * (S::STAGE_BYTES >> 4));
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
 #pragma unroll
           for (int i = 0; i < CL; ++i) sx[i] = __ldg(xs[i] + kb + 1);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(tfull_bar(a), (use / NBUF) & 1u, wc, SITE_TC_EPILOGUE));
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(tfull_bar(a), (use / NBUF) & 1u, wc, SITE_TC_EPILOGUE));
         if (!ok) break;
         tc_fence_after();
         uint32_t v[NC];

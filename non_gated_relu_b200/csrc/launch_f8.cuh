@@ -192,9 +192,9 @@ static nh_status run_f8(const F8Call& c, int dev, cudaStream_t st) {
   if (f8_gemv_rows(c)) return launch_f8_gemv(c, st);
   // Few rows: tiles of 128 features x 64 rows while each SM gets one at most, where
   // 256 x 256 tiles leave most SMs without.  Measured in a graph with the
-  // quantization, these against those: N 3712, K 2688: 12.2 and 14.8 us for 64 rows,
-  // 13.6 and 15.6 for 320 (145 tiles), 16.6 and 16.1 for 448 (203); N 512, K 4096,
-  // 100 rows: 16.2 and 19.6.
+  // quantization, these against those: N 3712, K 2688: 11.5 and 14.4 us for 64 rows,
+  // 12.8 and 15.3 for 320 (145 tiles), and 16.6 against 16.1 for 448 (203); N 512, K
+  // 4096, 100 rows: 16.4 and 18.9.
   const int64_t small = (c.rows + F8_DENSE_NT - 1) / F8_DENSE_NT * ((c.N + f8s::M - 1) / f8s::M);
   if (!c.tiles && small <= g_sm_count[dev]) return launch_f8_swap_as<F8_DENSE_NT, 4, 2>(c, dev, st);
   return launch_f8_pair(c, dev, st);
