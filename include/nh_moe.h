@@ -171,8 +171,9 @@ typedef struct {
     int32_t x_direct;     /* 1: the up projection reads x itself (no x_perm)    */
     /* With NH_WEIGHTS_FP8, written by the up projection's call: x_perm holds the
      * E4M3 codes of x [rows, H] in permuted order and behind them, 256-byte
-     * aligned, their scales float [rows, ceil(H / 128)]; h holds the codes of
-     * relu^2(up) [rows, I] and their scales.  x_direct is 0; swap_ab is 1 while
+     * aligned, their scales float [rows, ceil(H / 128)] and then, written by the down
+     * projection's call, its rows float [rows, H] before their weights; h holds the
+     * codes of relu^2(up) [rows, I] and their scales.  x_direct is 0; swap_ab is 1 while
      * an expert has few rows in the mean (tile entries of up to 64 rows). */
 } nh_moe_ws_layout;
 
@@ -516,8 +517,12 @@ nh_status nh_fp8_linear(int64_t T, int64_t N, int64_t K, const void *x, int32_t 
  * w_shared_up [1][S][H], w_shared_down [1][H][S].  x is quantized per (token, 128
  * features); relu^2 of the up projection is quantized the same way from its
  * float32 value (it is never rounded to bf16).  NaN passes through relu^2.
- * Everything else as there: the permute before, float32 adds into y_acc, the
- * routed workspace (nh_moe_ws_layout) and ws_shared (256-byte aligned).
+ * A token's k rows are weighted and summed in float32, in the order of its slots, and
+ * the sum is added to y_acc once; the shared expert adds once, too.  So results do
+ * not depend on scheduling (a y_acc that starts at zero and takes both adds
+ * included), unlike those of nh_moe_forward, whose adds into y_acc have no fixed
+ * order.  Everything else as there: the permute before, the routed workspace
+ * (nh_moe_ws_layout) and ws_shared (256-byte aligned).
  */
 nh_status nh_moe_forward_fp8(const nh_moe_config *cfg, int64_t T, const void *x,
                              const nh_fp8_weight *w_up, const nh_fp8_weight *w_down, void *ws,

@@ -121,8 +121,8 @@ static nh_status f8_experts_up(const Plan& p, int64_t T, const void* x, const nh
   return run_f8(c, dev, st);
 }
 
-static nh_status f8_experts_down(const Plan& p, const nh_fp8_weight* w, void* ws, float* y_acc,
-                                 bool follows, int dev, cudaStream_t st) {
+static nh_status f8_experts_down(const Plan& p, int64_t T, const nh_fp8_weight* w, void* ws,
+                                 float* y_acc, bool follows, int dev, cudaStream_t st) {
   const nh_moe_ws_layout& L = p.lay;
   const F8Hidden h = f8_hidden(at<void>(ws, L.h), p.rows, p.I);
   F8Call c{};
@@ -138,13 +138,14 @@ static nh_status f8_experts_down(const Plan& p, const nh_fp8_weight* w, void* ws
   c.num_tiles = at<int32_t>(ws, L.num_tiles);
   c.max_tiles = L.max_tiles;
   c.tile_rows = L.tile_rows;
-  c.out_kind = F8_COMBINE;
-  c.out = y_acc;
-  c.perm_w = at<float>(ws, L.perm_w);
-  c.dst_row = at<int32_t>(ws, L.perm_token);
+  float* rows = at<float>(ws, f8_down_rows_at(p));
+  c.out_kind = F8_F32;
+  c.out = rows;
   c.status = at<int>(ws, L.status);
   c.early_w = follows;
-  return run_f8(c, dev, st);
+  NH_TRY(run_f8(c, dev, st));
+  return launch_combine(rows, at<int32_t>(ws, L.inv_row), at<float>(ws, L.perm_w), T, p.k, p.H,
+                        y_acc, st);
 }
 
 static nh_status f8_experts(const nh_moe_config* cfg, int64_t T, const void* x,
@@ -165,7 +166,7 @@ static nh_status f8_experts(const nh_moe_config* cfg, int64_t T, const void* x,
   NH_TRY(device_setup(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (up) NH_TRY(f8_experts_up(p, T, x, w_up, ws, dev, st));
-  if (down) NH_TRY(f8_experts_down(p, w_down, ws, y_acc, up, dev, st));
+  if (down) NH_TRY(f8_experts_down(p, T, w_down, ws, y_acc, up, dev, st));
   return NH_OK;
 }
 

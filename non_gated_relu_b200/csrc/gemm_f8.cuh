@@ -63,8 +63,7 @@ enum Out : int {
   OUT_BF16 = 0,        // out bf16 [rows, N] = acc
   OUT_F32 = 1,         // out f32 [rows, N] = acc
   OUT_RELU2_F8 = 2,    // out E4M3 [rows, N] of relu(acc)^2, scales [rows, ceil(N / 128)]
-  OUT_ADD_F32 = 3,     // out f32 [rows, N] += acc, atomic adds
-  OUT_COMBINE = 4,     // out f32: out[dst_row[r]] += perm_w[r] * acc, atomic adds
+  OUT_ADD_F32 = 3,     // out f32 [rows, N] += acc, atomic adds (one to an element)
 };
 
 struct Args {
@@ -77,8 +76,6 @@ struct Args {
   void* out;
   float* out_scales;       // OUT_RELU2_F8
   int64_t ldo;
-  const float* perm_w;
-  const int32_t* dst_row;
   int* status;
   uint64_t timeout_ns;
 };
@@ -220,20 +217,15 @@ __device__ __forceinline__ uint32_t relu_amax(int n, float (&acc)[COLS]) {
 template <int OUT>
 __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, int f0, int n,
                                             float (&acc)[COLS], uint4* stage, int lane) {
-  constexpr bool F32 = OUT == OUT_F32 || OUT == OUT_ADD_F32 || OUT == OUT_COMBINE;
+  constexpr bool F32 = OUT == OUT_F32 || OUT == OUT_ADD_F32;
   constexpr int PER = F32 ? 4 : (OUT == OUT_BF16 ? 8 : 16);   // features of a 16-byte word
   constexpr int PASSES = COLS / (8 * PER);
-  const int mine = row0 + min(lane, rows - 1);
-  int64_t to = mine;      // output row of this lane's row
-  float w = 1.f;
-  if constexpr (OUT == OUT_COMBINE) {
-    to = g.dst_row[mine];
-    w = g.perm_w[mine];
-  }
+  float w = 1.f;          // OUT_RELU2_F8: one over the row's scale
   if constexpr (OUT == OUT_RELU2_F8) {
     const int e = f8::scale_exp(relu_amax(n, acc));
     w = f8::pow2(-e);
-    if (lane < rows) g.out_scales[(size_t)mine * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
+    if (lane < rows)
+      g.out_scales[(size_t)(row0 + lane) * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
   }
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
@@ -243,8 +235,8 @@ __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, i
       const int c = (p * 8 + j) * PER;
       uint4 word;
       if constexpr (F32) {
-        word = make_uint4(__float_as_uint(w * acc[c]), __float_as_uint(w * acc[c + 1]),
-                          __float_as_uint(w * acc[c + 2]), __float_as_uint(w * acc[c + 3]));
+        word = make_uint4(__float_as_uint(acc[c]), __float_as_uint(acc[c + 1]),
+                          __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3]));
       } else if constexpr (OUT == OUT_BF16) {
         word = make_uint4(pack_bf16x2(acc[c], acc[c + 1]), pack_bf16x2(acc[c + 2], acc[c + 3]),
                           pack_bf16x2(acc[c + 4], acc[c + 5]), pack_bf16x2(acc[c + 6], acc[c + 7]));
@@ -262,10 +254,9 @@ __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, i
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
       const uint4 word = stage[r * 8 + (j ^ (r & 7))];
-      const int64_t row = OUT == OUT_COMBINE ? __shfl_sync(0xffffffffu, (int)to, r) : row0 + r;
       if (r < rows && c < n) {
-        const size_t at = (size_t)row * g.ldo + f0 + c;
-        if constexpr (OUT == OUT_ADD_F32 || OUT == OUT_COMBINE)
+        const size_t at = (size_t)(row0 + r) * g.ldo + f0 + c;
+        if constexpr (OUT == OUT_ADD_F32)
           red_add_f32x4(static_cast<float*>(g.out) + at, __uint_as_float(word.x),
                         __uint_as_float(word.y), __uint_as_float(word.z), __uint_as_float(word.w));
         else if constexpr (OUT == OUT_F32)

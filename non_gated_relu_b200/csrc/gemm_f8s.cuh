@@ -24,7 +24,7 @@
 // weights before it waits for it (they were there before), which covers launch
 // and tail.
 //
-// The end of a tile: the combine adds 32 neighbouring features of a row per
+// The end of a tile: a warp stores 32 neighbouring features of a row per
 // instruction; relu^2 needs the maximum over the tile's 128 features, which lie
 // in four warps: they exchange column maxima and then codes through shared
 // memory, in two bounded barrier waits, and store whole 128-byte rows.
@@ -45,10 +45,9 @@ constexpr int NBUF = 4;            // accumulators
 
 enum Out : int {
   OUT_RELU2_F8 = 0,  // out E4M3 [rows, N] of relu(acc)^2, scales [rows, ceil(N / 128)]
-  OUT_COMBINE = 1,   // out f32: out[dst_row[r]] += perm_w[r] * acc, atomic adds
-  OUT_BF16 = 2,      // out bf16 [rows, N] = acc
-  OUT_F32 = 3,       // out f32 [rows, N] = acc
-  OUT_ADD_F32 = 4,   // out f32 [rows, N] += acc, atomic adds
+  OUT_BF16 = 1,      // out bf16 [rows, N] = acc
+  OUT_F32 = 2,       // out f32 [rows, N] = acc
+  OUT_ADD_F32 = 3,   // out f32 [rows, N] += acc, atomic adds (one to an element)
 };
 
 struct Args {
@@ -60,8 +59,6 @@ struct Args {
   int N, K, KB;
   void* out;
   float* out_scales;       // OUT_RELU2_F8
-  const float* perm_w;     // OUT_COMBINE
-  const int32_t* dst_row;
   int* status;
   uint64_t timeout_ns;
   int early_w;             // weights and tile table were complete before the
@@ -337,23 +334,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       if (!ok) break;
       const int cols = min(NC, ent.z - half * NC);         // <= 0: none in this half
       const int f = t.nb * M + quarter * 32 + lane;        // this lane's feature
-      if constexpr (OUT == OUT_COMBINE) {
-        float wt[CL];
-        int to[CL];
-#pragma unroll
-        for (int i = 0; i < CL; ++i) {
-          const int r = ent.y + min(half * NC + min(lane + 32 * i, NC - 1), ent.z - 1);
-          wt[i] = g.perm_w[r];
-          to[i] = g.dst_row[r];
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float w = __shfl_sync(0xffffffffu, wt[c / 32], c & 31);
-          const int row = __shfl_sync(0xffffffffu, to[c / 32], c & 31);
-          if (c < cols && f < g.N)
-            red_add_f32(static_cast<float*>(g.out) + (size_t)row * g.N + f, w * acc[c]);
-        }
-      } else if constexpr (OUT != OUT_RELU2_F8) {
+      if constexpr (OUT != OUT_RELU2_F8) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
           if (c < cols && f < g.N) {

@@ -24,7 +24,7 @@ static nh_status check_f8(const nh_fp8_weight* w, const char* name) {
 }
 
 // One product: out = outkind(x W[e]^T) over tile entries or dense rows.
-enum F8Out { F8_BF16, F8_F32, F8_RELU2, F8_ADD, F8_COMBINE };
+enum F8Out { F8_BF16, F8_F32, F8_RELU2, F8_ADD };
 struct F8Call {
   const uint8_t* x;          // codes [x_rows, K]
   const float* xs;
@@ -40,8 +40,6 @@ struct F8Call {
   F8Out out_kind;
   void* out;                 // F8_RELU2: codes, or float32 from the GEMV
   float* out_scales;         // F8_RELU2: their scales (not the GEMV)
-  const float* perm_w;
-  const int32_t* dst_row;
   int* status;
   bool early_w;
 };
@@ -62,8 +60,7 @@ static nh_status launch_f8_gemv(const F8Call& c, cudaStream_t st, const void* x 
     case F8_BF16: a.out_kind = f8v::OUT_BF16; break;
     case F8_F32: a.out_kind = f8v::OUT_F32; break;
     case F8_RELU2: a.out_kind = f8v::OUT_RELU2_F32; break;
-    case F8_ADD: a.out_kind = f8v::OUT_ADD_F32; break;
-    default: return fail(NH_ERR_UNSUPPORTED, "internal: the FP8 GEMV has no combine");
+    default: a.out_kind = f8v::OUT_ADD_F32;
   }
   a.out = c.out;
   a.early_w = c.early_w ? 1 : 0;
@@ -92,8 +89,6 @@ static nh_status launch_f8_swap_as(const F8Call& c, int dev, cudaStream_t st) {
   a.KB = (int)f8_blocks(c.K);
   a.out = c.out;
   a.out_scales = c.out_scales;
-  a.perm_w = c.perm_w;
-  a.dst_row = c.dst_row;
   a.status = c.status;
   a.timeout_ns = timeout_ns();
   a.early_w = c.early_w ? 1 : 0;
@@ -104,15 +99,12 @@ static nh_status launch_f8_swap_as(const F8Call& c, int dev, cudaStream_t st) {
   if (c.out_kind == F8_RELU2)
     return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_RELU2_F8>, grid,
                     dim3(f8s::THREADS), S::SMEM, st, mx, mw, a);
-  if (c.out_kind == F8_COMBINE)
-    return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_COMBINE>, grid,
+  if (c.out_kind == F8_F32)
+    return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_F32>, grid,
                     dim3(f8s::THREADS), S::SMEM, st, mx, mw, a);
   if constexpr (NT == F8_DENSE_NT) {
     if (c.out_kind == F8_BF16)
       return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_BF16>, grid,
-                      dim3(f8s::THREADS), S::SMEM, st, mx, mw, a);
-    if (c.out_kind == F8_F32)
-      return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_F32>, grid,
                       dim3(f8s::THREADS), S::SMEM, st, mx, mw, a);
     return launch_k("f8_swap_gemm", f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_ADD_F32>, grid,
                     dim3(f8s::THREADS), S::SMEM, st, mx, mw, a);
@@ -169,8 +161,6 @@ static nh_status launch_f8_pair(const F8Call& c, int dev, cudaStream_t st) {
   a.out = c.out;
   a.out_scales = c.out_scales;
   a.ldo = c.N;
-  a.perm_w = c.perm_w;
-  a.dst_row = c.dst_row;
   a.status = c.status;
   a.timeout_ns = timeout_ns();
   const int64_t m = c.tiles ? c.max_tiles : (c.rows + f8g::MP - 1) / f8g::MP;
@@ -179,8 +169,7 @@ static nh_status launch_f8_pair(const F8Call& c, int dev, cudaStream_t st) {
     case F8_BF16: return launch_f8_pair_as<f8g::OUT_BF16>(c, a, tiles, dev, st);
     case F8_F32: return launch_f8_pair_as<f8g::OUT_F32>(c, a, tiles, dev, st);
     case F8_RELU2: return launch_f8_pair_as<f8g::OUT_RELU2_F8>(c, a, tiles, dev, st);
-    case F8_ADD: return launch_f8_pair_as<f8g::OUT_ADD_F32>(c, a, tiles, dev, st);
-    default: return launch_f8_pair_as<f8g::OUT_COMBINE>(c, a, tiles, dev, st);
+    default: return launch_f8_pair_as<f8g::OUT_ADD_F32>(c, a, tiles, dev, st);
   }
 }
 
@@ -222,6 +211,18 @@ static F8Hidden f8_hidden(void* base, int64_t R, int64_t C) {
   char* b = static_cast<char*>(base);
   return {reinterpret_cast<uint8_t*>(b), reinterpret_cast<float*>(b + f8_scales_at(R, C)),
           reinterpret_cast<float*>(b + f8_rows_bytes(R, C))};
+}
+
+// Rows of the down projection, weighted and summed per token, into y_acc.
+static nh_status launch_combine(const float* rows, const int32_t* inv_row, const float* perm_w,
+                                int64_t T, int k, int H, float* y_acc, cudaStream_t st) {
+  const int quads = H / 4;                        // H is a multiple of 64
+  const int parts = (quads + 255) / 256;          // blocks of a token
+  const int threads = ((quads + parts - 1) / parts + 31) / 32 * 32;
+  if (T > 0x7fffffff / parts)
+    return fail(NH_ERR_UNSUPPORTED, "combine of %lld tokens", (long long)T);
+  return launch_k("combine_rows", f8::combine_rows, dim3((unsigned)(T * parts)), dim3(threads), 0, st,
+                  rows, inv_row, perm_w, parts, k, quads, y_acc);
 }
 
 // A dense product of unquantized rows: in one launch up to F8_RAW_ROWS of them,

@@ -238,7 +238,7 @@ static nh_status make_plan(const nh_moe_config* c, int64_t T, Plan* p) {
   L.num_tiles = take(4);
   if (c->weight_format == NH_WEIGHTS_FP8) {
     L.x_direct = 0;
-    L.x_perm = take(f8_rows_bytes(rows, p->H));
+    L.x_perm = take(f8_rows_bytes(rows, p->H) + (size_t)rows * p->H * 4);
     L.h = take(f8_rows_bytes(rows, p->I));
   } else {
     L.x_perm = take(L.x_direct ? 0 : (size_t)rows * p->H * p->elem);
@@ -255,6 +255,9 @@ static nh_status check_ptr(const void* p, const char* name) {
     return fail(NH_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
   return NH_OK;
 }
+
+// FP8: the down projection's rows, float [rows, H], behind the quantized x
+static size_t f8_down_rows_at(const Plan& p) { return p.lay.x_perm + f8_rows_bytes(p.rows, p.H); }
 
 static nh_status check_ws(const Plan& p, void* ws, size_t ws_bytes) {
   NH_TRY(check_ptr(ws, "ws"));
@@ -347,12 +350,10 @@ static nh_status f8_swap_attrs() {
   constexpr int smem = f8s::Shape<NT, STAGES, CTAS>::SMEM;
   NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_RELU2_F8>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_COMBINE>,
+  NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_F32>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if constexpr (NT == F8_DENSE_NT) {
     NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_BF16>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_F32>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     NH_CUDA(cudaFuncSetAttribute(f8s::f8_swap_gemm<NT, STAGES, CTAS, f8s::OUT_ADD_F32>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -393,7 +394,6 @@ static nh_status set_attrs(int dev) {
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_F32>));
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_RELU2_F8>));
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_ADD_F32>));
-  NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_COMBINE>));
   NH_TRY((f8_swap_attrs<16, 5, 2>()));
   NH_TRY((f8_swap_attrs<32, 5, 2>()));
   NH_TRY((f8_swap_attrs<64, 4, 2>()));
@@ -415,7 +415,7 @@ static nh_status set_attrs(int dev) {
     g_pair_clusters[dev] = n;
     lc.blockDim = dim3(f8g::THREADS, 1, 1);
     lc.dynamicSmemBytes = f8g::SMEM;
-    NH_CUDA(cudaOccupancyMaxActiveClusters(&n, f8g::f8_pair_gemm<f8g::OUT_COMBINE>, &lc));
+    NH_CUDA(cudaOccupancyMaxActiveClusters(&n, f8g::f8_pair_gemm<f8g::OUT_F32>, &lc));
     if (n < 1) return fail(NH_ERR_UNSUPPORTED, "no 2-CTA cluster of the FP8 GEMM fits on device %d", dev);
     g_f8_clusters[dev] = n;
   }

@@ -734,3 +734,79 @@ def test_weights_quantized_here_serve_the_block():
     ya, yb = a.forward(x).double(), b.forward(x).double()
     # five roundings to E4M3 a path (x, W_up twice through the square, h, W_down), 2^-4 each
     assert ((ya - yb).norm() / ya.norm()).item() <= 5 * 2.0 ** -4
+
+
+# -- repeated calls ----------------------------------------------------------------------
+@pytest.mark.parametrize("T,kw", [
+    (1, {}), (8, {}), (32, {}), (33, {}), (301, {}), (1500, {}),
+    (4000, dict(n_routed_experts=8, n_group=1, topk_group=1, num_experts_per_tok=6)),
+    (700, dict(n_routed_experts=64, n_group=1, topk_group=1, num_experts_per_tok=20))])
+def test_experts_repeat_bit_for_bit(T, kw):
+    """A token's k rows meet in the order of its slots, whatever order the tiles end in: the
+    same bits from every call, also beside a call on another stream, and in a graph."""
+    gen = generator(T + 7)
+    cfg = config(T, **kw)
+    c = nh.config_from(cfg)
+    up, down = experts_case(cfg, gen)
+    fu, fd = nh.fp8_weight(*up), nh.fp8_weight(*down)
+    idx, w = routing(T, cfg.E, cfg.k, gen, skew=1.0)
+    x = torch.randn((T, cfg.H), generator=gen, device=DEV).to(B16)
+    sets = [(torch.zeros(nh.workspace_size(c, T), dtype=torch.uint8, device=DEV),
+             torch.zeros((T, cfg.H), device=DEV)) for _ in range(2)]
+
+    def go(ws, y, stream=None):
+        nh.zero_acc(c, T, y, stream=stream)
+        nh.permute(c, x, idx, w, ws, stream=stream)
+        nh.forward_fp8(c, x, fu, fd, ws, y, stream=stream)
+
+    go(*sets[0])
+    want = sets[0][1].clone()
+    assert want.abs().amax() > 0
+    for _ in range(8):
+        go(*sets[0])
+        assert torch.equal(sets[0][1], want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(8):
+        for (ws, y), st in zip(sets, streams):
+            go(ws, y, st)
+    torch.cuda.synchronize()
+    for ws, y in sets:
+        assert nh.check_device(ws) == 0 and torch.equal(y, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go(*sets[0])
+    for _ in range(4):
+        sets[0][1].fill_(3.0)
+        g.replay()
+        assert torch.equal(sets[0][1], want)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T", [8, 32, 40, 700])
+def test_block_repeats_bit_for_bit(T, score):
+    """Routed and shared expert add once each to an accumulator that starts at zero (or the
+    routed one to the shared one's values): no order between them changes a bit."""
+    cfg = config(T, scoring_func=score)
+    blk, *_, gen = block_and_parts(cfg, T, bias=True)
+    x = torch.randn((T, cfg.H), generator=gen, device=DEV).to(B16)
+    want = blk.forward(x, partial=True).clone()
+    for _ in range(10):
+        assert torch.equal(blk.forward(x, partial=True), want)
+    assert blk.check(T) == 0
+
+
+def test_experts_add_to_what_is_there():
+    gen = generator(77)
+    for T in (3, 200, 1500):
+        cfg = config(T)
+        c = nh.config_from(cfg)
+        up, down = experts_case(cfg, gen)
+        idx, w = routing(T, cfg.E, cfg.k, gen)
+        x = torch.randn((T, cfg.H), generator=gen, device=DEV).to(B16)
+        alone, *_ = run_experts(cfg, x, idx, w, up, down)
+        start = torch.randn((T, cfg.H), generator=gen, device=DEV)
+        y, ws = start.clone(), torch.zeros(nh.workspace_size(c, T), dtype=torch.uint8, device=DEV)
+        nh.permute(c, x, idx, w, ws)
+        nh.forward_fp8(c, x, nh.fp8_weight(*up), nh.fp8_weight(*down), ws, y)
+        assert torch.equal(y, start + alone)      # one float32 add
