@@ -195,14 +195,41 @@ __device__ __forceinline__ void top2_add(V v, V& v1, V& v2) {
   }
 }
 
+// How far the exact value of a group may lie from its float32 value gs: tol_s for the
+// scores, and half a unit in the last place of either c and of their sum, 2^-23 (|v1| +
+// |v2|) together.  The sum of two of opposite sign is small where its error is not, so
+// each group brings its own error, and a kept group is certain only if it stays above
+// every dropped one.  2^-22 covers the rounding of gs +- e, too.  A group without a
+// usable expert is exactly -inf; one past float32's range is never certain.
+struct Reach {
+  float lo, hi;
+  __device__ __forceinline__ Reach(float gs, float v1, float v2, bool top2, float tol_s) {
+    const float size = fabsf(v1) + (top2 && v2 != -INFINITY ? fabsf(v2) : 0.f);
+    const float e = tol_s + 0x1p-22f * size;
+    lo = gs - e;
+    hi = gs + e;
+    if (v1 == -INFINITY) {
+      lo = INFINITY;
+      hi = -INFINITY;
+    } else if (!(size < INFINITY)) {
+      lo = -INFINITY;
+      hi = INFINITY;
+    }
+  }
+};
+// Is the lowest end of the kept groups (lo) not above the highest of the dropped (hi)?
+__device__ __forceinline__ bool overlap(float kept_lo, float dropped_hi) {
+  return !(-warp_max(-kept_lo) > warp_max(dropped_hi));
+}
+
 // Groups by value from shared memory, any group size: lane q reduces groups q
 // and q + 32, starting at its own place in the group so that the lanes' reads
 // spread over the banks.  Returns the kept groups as a mask; `close` (float)
-// is set where the last group kept and the first one dropped are within tol.
+// is set where a kept and a dropped group are within their errors (Reach).
 template <typename V>
 __device__ __forceinline__ uint64_t keep_groups(const V* c, int G, int g, int tg, bool top2,
                                                 int lane, float tol_s, bool* close) {
-  V gs[2];
+  V gs[2], v1s[2], v2s[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int q = lane + 32 * r;
@@ -213,6 +240,8 @@ __device__ __forceinline__ uint64_t keep_groups(const V* c, int G, int g, int tg
         if (++p == g) p = 0;
       }
     gs[r] = group_value(v1, v2, top2);
+    v1s[r] = v1;
+    v2s[r] = v2;
   }
   int rank[2] = {0, 0};
   for (int q = 0; q < G; ++q) {
@@ -227,21 +256,18 @@ __device__ __forceinline__ uint64_t keep_groups(const V* c, int G, int g, int tg
 #pragma unroll
   for (int r = 0; r < 2; ++r)
     keep |= (uint64_t)__ballot_sync(FULL, lane + 32 * r < G && rank[r] < tg) << (32 * r);
-  if (close && tg < G) {
-    // values of ranks tg - 1 and tg
-    V last = 0, next = 0;
+  if (close) {
+    float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const bool in = lane + 32 * r < G;
-      const unsigned a = __ballot_sync(FULL, in && rank[r] == tg - 1);
-      const unsigned b = __ballot_sync(FULL, in && rank[r] == tg);
-      const V va = __shfl_sync(FULL, gs[r], a ? __ffs(a) - 1 : 0);
-      const V vb = __shfl_sync(FULL, gs[r], b ? __ffs(b) - 1 : 0);
-      if (a) last = va;
-      if (b) next = vb;
+      if (lane + 32 * r >= G) continue;
+      const Reach at((float)gs[r], (float)v1s[r], (float)v2s[r], top2, tol_s);
+      if (rank[r] < tg)
+        lo = fminf(lo, at.lo);
+      else
+        hi = fmaxf(hi, at.hi);
     }
-    // two group values that are both -inf tie exactly; a sum of two may be +inf
-    *close = last != -INFINITY && !((float)(last - next) > tol_s + 0x1p-22f * fabsf((float)last));
+    *close = overlap(lo, hi);
   }
   return keep;
 }
@@ -470,12 +496,11 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
         const float o = __shfl_sync(FULL, gs, q * width);
         rank += (o > gs || (o == gs && q < me)) ? 1 : 0;
       }
-      const bool in = me < a.G;
-      const unsigned la = __ballot_sync(FULL, in && rank == a.tg - 1);
-      const unsigned lb = __ballot_sync(FULL, in && rank == a.tg);
-      const float last = __shfl_sync(FULL, gs, __ffs(la) - 1);
-      const float next = __shfl_sync(FULL, gs, __ffs(lb) - 1);
-      close = last != -INFINITY && !(last - next > 2.f * tol_s + 0x1p-22f * fabsf(last));
+      if (by_score) {
+        const Reach at(gs, v1, v2, a.top2, tol_s);
+        close = overlap(me < a.G && rank < a.tg ? at.lo : INFINITY,
+                        me < a.G && rank >= a.tg ? at.hi : -INFINITY);
+      }
       if (rank >= a.tg) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) key[i] = 0u;
@@ -487,13 +512,13 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
         if (e0 + i < E) cs[e0 + i] = c[i];
       __syncwarp();
       const uint64_t keep =
-          keep_groups<float>(cs, a.G, g, a.tg, a.top2, lane, 2.f * tol_s, &close);
+          keep_groups<float>(cs, a.G, g, a.tg, a.top2, lane, tol_s, by_score ? &close : nullptr);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (e0 + i < E && !((keep >> ((e0 + i) / g)) & 1ull)) key[i] = 0u;
     }
-    again = by_score && close;
+    again = close;
   }
 
   // the k best, lane j the j-th; with scores one more, whose distance counts

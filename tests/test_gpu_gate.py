@@ -164,6 +164,72 @@ def test_no_tokens():
     run(torch.empty((0, 16), device=DEV), None, 1, 1, 2, True, True, False)
 
 
+def choose_exact(logits, bias, G, tg, k, softmax):
+    """The choice by groups of two from scores in 64 bits, whole batches at once."""
+    l = logits.double()
+    c = (torch.softmax(l, 1) if softmax else torch.sigmoid(l)) + bias.double()
+    T, E = c.shape
+    value = c.view(T, G, E // G).topk(2, dim=2).values.sum(dim=2)
+    order = value.sort(dim=1, descending=True, stable=True).indices[:, :tg]
+    keep = torch.zeros((T, G), dtype=torch.bool, device=DEV).scatter_(1, order, True)
+    c = c.masked_fill(~keep.repeat_interleave(E // G, dim=1), -math.inf)
+    return c.sort(dim=1, descending=True, stable=True).indices[:, :k]
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("size", [4.0, 16.0, 64.0, 1024.0, 2.0 ** 20])
+@pytest.mark.parametrize("g", [2, 3])
+def test_near_groups_with_biases_of_mixed_sign(softmax, size, g):
+    """Two groups whose two best have biases of opposite sign: sums within 1e-5, each of two
+    float32 values that were rounded at the size of their biases."""
+    gen = torch.Generator(device=DEV).manual_seed(int(size) + g)
+    T = 200000
+    u = torch.rand((T, 3), generator=gen, device=DEV).double() * 0.4 + 0.3
+    near = (torch.rand(T, generator=gen, device=DEV).double() - 0.5) * 2e-5
+    u = torch.cat([u, (u[:, 0] + u[:, 1] - u[:, 2] + near)[:, None]], dim=1)
+    ok = (u[:, 3] > 0.05) & (u[:, 3] < 0.95)
+    l = (torch.log(u) if softmax else torch.logit(u))[ok].float()
+    logits = torch.full((l.shape[0], 2 * g), -3.0, device=DEV)
+    at = torch.tensor([0, 1, g, g + 1], device=DEV)
+    logits[:, at] = l
+    bias = torch.full((2 * g,), -4.0 * size - 8, device=DEV)
+    bias[at] = torch.tensor([1.0, -1.0, 1.37, -1.37], device=DEV) * size
+    _, idx, _ = run(logits, bias, 2, 1, 2, softmax, True, True)
+    want = choose_exact(logits, bias, 2, 1, 2, softmax)
+    bad = (idx != want).any(dim=1)
+    assert not bad.any(), (int(bad.sum()), idx[bad][:3], want[bad][:3])
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("E,G,tg", [(64, 8, 4), (64, 8, 1), (60, 10, 3), (128, 64, 9), (512, 64, 20),
+                                    (256, 8, 4)])
+def test_groups_with_errors_of_different_size(softmax, E, G, tg):
+    """Biases of mixed sign, other sizes in each group: the group that float32 misjudges need
+    not be the first one dropped."""
+    gen = torch.Generator(device=DEV).manual_seed(E + G + tg)
+    g, T = E // G, 60000
+    logits = torch.randn((T, E), generator=gen, device=DEV)
+    size = torch.exp2(torch.randint(0, 15, (G,), generator=gen, device=DEV).float())
+    size *= 1 + torch.rand(G, generator=gen, device=DEV)
+    bias = torch.full((G, g), -2.0 ** 17, device=DEV)
+    bias[:, 0], bias[:, -1] = -size, size
+    _, idx, _ = run(logits, bias.view(-1), G, tg, min(2 * tg, 32), softmax, True, True)
+    want = choose_exact(logits, bias.view(-1), G, tg, min(2 * tg, 32), softmax)
+    bad = (idx != want).any(dim=1)
+    assert not bad.any(), (int(bad.sum()), idx[bad][:3], want[bad][:3])
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_group_sums_past_either_end_of_float32(sign):
+    gen = torch.Generator(device=DEV).manual_seed(19)
+    for E, G, tg in ((8, 4, 2), (12, 4, 1), (64, 32, 5)):
+        x = torch.randn((40, E), generator=gen, device=DEV)
+        x[:8, : E // G] = -math.inf
+        for _ in range(3):
+            b = sign * 2.5e38 * (1 + torch.rand(E, generator=gen, device=DEV) * 0.25)
+            check(x, b, G, tg, 2, False, True, True)
+
+
 # -- gradient ---------------------------------------------------------------------------
 def reference_gradient(logits, idx, dw, softmax, norm, alpha):
     l = ref.clean(logits).requires_grad_(True)
