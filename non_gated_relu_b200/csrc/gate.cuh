@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (e0 + i < E) c[i] += __ldg(a.bias + e0 + i);
+        if (l[i] != -INFINITY) c[i] += __ldg(a.bias + e0 + i);   // past E, too, l is -inf
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] += 0.0f;

@@ -230,6 +230,22 @@ def test_group_sums_past_either_end_of_float32(sign):
             check(x, b, G, tg, 2, False, True, True)
 
 
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("G,tg", [(1, 1), (4, 2)])
+def test_an_infinite_bias_does_not_raise_a_masked_expert(softmax, G, tg):
+    """-inf logits stay -inf whatever their bias (+inf is not of the documented values)."""
+    gen = torch.Generator(device=DEV).manual_seed(23)
+    E, k = 32, 4
+    x = torch.randn((64, E), generator=gen, device=DEV)
+    masked = torch.rand((64, E), generator=gen, device=DEV) < 0.3
+    masked[:, ::8] = True
+    x[masked] = -math.inf
+    b = torch.zeros(E, device=DEV)
+    b[::8], b[1::16] = math.inf, math.inf
+    _, idx, w = run(x, b, G, tg, k, softmax, True, True)
+    assert not masked.gather(1, idx).any() and (w > 0).all()
+
+
 # -- gradient ---------------------------------------------------------------------------
 def reference_gradient(logits, idx, dw, softmax, norm, alpha):
     l = ref.clean(logits).requires_grad_(True)
