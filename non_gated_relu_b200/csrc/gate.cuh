@@ -620,15 +620,19 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
   }
 }
 
-// d logits from d weights.  With p_j the shares of the chosen experts and D =
-// sum p_j dw_j:
-//   norm, softmax   dl_j = alpha p_j (dw_j - D)
-//   norm, sigmoid   dl_j = alpha p_j (dw_j - D) (1 - s_j)
+// d logits from d weights.  With p_j the shares of the chosen experts, s the scores,
+// and for raw softmax r the summed score of the experts not chosen:
+//   norm, softmax   dl_j = alpha p_j sum_i p_i (dw_j - dw_i)
+//   norm, sigmoid   the same times (1 - s_j)
 //   raw,  sigmoid   dl_j = alpha dw_j s_j (1 - s_j)
-//   raw,  softmax   dl_i = alpha s_i ([i chosen] dw_i - sum_j s_j dw_j), every i
-// (from dw = alpha d(s_j / sum s): d log p_j = d log s_j - sum p d log s).  An
-// expert named twice gets both parts, in slot order; an id outside [0, E)
-// takes no part.  One write of each row, and its read only for raw softmax.
+//   raw,  softmax   dl_j = alpha s_j (r dw_j + sum_i s_i (dw_j - dw_i)), j chosen
+//                   dl_n = -alpha s_n sum_i s_i dw_i, the others
+// (from dw = alpha d(s_j / sum s): d log p_j = d log s_j - sum p d log s).  The sums
+// over differences are dw_j - sum p dw and dw_j - sum s dw without their cancellation:
+// where one expert has nearly all of the weight, those lose every digit of its
+// gradient.  An expert named twice gets both parts, in slot order (with raw softmax its
+// dw are summed first); an id outside [0, E) takes no part.  One write of each row, and
+// its read only for raw softmax.
 template <int PER, typename Tin>
 __global__ void __launch_bounds__(WARPS * 32) gate_backward(const Args a) {
   pdl_wait();
@@ -655,8 +659,10 @@ __global__ void __launch_bounds__(WARPS * 32) gate_backward(const Args a) {
   float d;
   if (a.norm) {
     const float p = share(lj, a.softmax != 0);
-    const float mean = warp_sum(e >= 0 ? p * dw : 0.f);
-    d = a.alpha * p * (dw - mean);
+    float sum = 0.f;
+    for (int j = 0; j < k; ++j)
+      sum = fmaf(__shfl_sync(FULL, p, j), dw - __shfl_sync(FULL, dw, j), sum);
+    d = a.alpha * p * sum;
     if (!a.softmax) d *= sigmoid(-lj);
   } else if (!a.softmax) {
     d = a.alpha * dw * sigmoid(lj) * sigmoid(-lj);
@@ -668,19 +674,42 @@ __global__ void __launch_bounds__(WARPS * 32) gate_backward(const Args a) {
     for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
     float top = warp_max(m);
     if (top == -INFINITY) top = 0.f;
-    float p = 0.f;
+    // slots of the same expert are one, the first of them
+    uint32_t chosen = 0;
+    float w = 0.f;
+    bool first = e >= 0;
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl_sync(FULL, e, j);
+      const float dwj = __shfl_sync(FULL, dw, j);
+      if (ej == e) {
+        w += dwj;
+        first = first && j >= lane;
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i == ej) chosen |= 1u << i;
+    }
+    float p = 0.f, others = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       out[i] = expf(l[i] - top);
       p += out[i];
+      if (!((chosen >> i) & 1u)) others += out[i];
     }
     float z = warp_sum(p);
     if (z == 0.f) z = 1.f;
-    const float s = expf(lj - top) / z;
-    const float sum = warp_sum(e >= 0 ? s * dw : 0.f);
+    const float r = warp_sum(others) / z;
+    const float s = first ? expf(lj - top) / z : 0.f;
+    float sum = r * w, all = 0.f;
+    for (int j = 0; j < k; ++j) {
+      const float sj = __shfl_sync(FULL, s, j), wj = __shfl_sync(FULL, w, j);
+      sum = fmaf(sj, w - wj, sum);
+      all = fmaf(sj, wj, all);
+    }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) out[i] = -a.alpha * (out[i] / z) * sum;
-    d = a.alpha * s * dw;
+    for (int i = 0; i < PER; ++i)
+      out[i] = (chosen >> i) & 1u ? 0.f : -a.alpha * (out[i] / z) * all;
+    d = a.alpha * s * sum;
   }
   for (int j = 0; j < k; ++j) {
     const int ej = __shfl_sync(FULL, e, j);

@@ -254,6 +254,114 @@ def reference_gradient(logits, idx, dw, softmax, norm, alpha):
     return l.grad
 
 
+def gradient_and_size(logits, idx, dw, softmax, norm, alpha):
+    """Gradient in 64 bits by sums over differences, which cancel nowhere, and the size of
+    its terms: (d, size, slack), [T, E] each.  With raw softmax the dw of an expert that is
+    named m times are added first: m - 1 roundings of at most their magnitudes, which enter
+    the differences as they are, however small those come out (slack)."""
+    l, dw = ref.clean(logits), dw.double()
+    T, E = l.shape
+    k = idx.shape[1]
+    p = ref.gate_weights(l, idx, softmax, norm)                    # [T, k]
+    zero = torch.zeros_like(l)
+    if norm or not softmax:
+        if norm:
+            diff = dw[:, :, None] - dw[:, None, :]
+            parts = p[:, :, None] * p[:, None, :] * diff
+            d, size = parts.sum(dim=2), parts.abs().sum(dim=2)
+            if not softmax:
+                d, size = (v * torch.sigmoid(-l.gather(1, idx)) for v in (d, size))
+        else:
+            d = p * torch.sigmoid(-l.gather(1, idx)) * dw
+            size = d.abs()
+        return alpha * zero.scatter_add(1, idx, d), alpha * zero.scatter_add(1, idx, size), zero
+    s = torch.softmax(l, 1)
+    w, w_size = zero.scatter_add(1, idx, dw), zero.scatter_add(1, idx, dw.abs())
+    taken = torch.zeros_like(l, dtype=torch.bool).scatter_(1, idx, True)
+    sc = torch.where(taken, s, 0.0)
+    r = torch.where(taken, 0.0, s).sum(dim=1, keepdim=True)
+    adds = (zero.scatter_add(1, idx, torch.ones_like(dw)) - 1).clamp(min=0)
+    w_err = adds * 2.0 ** -24 * w_size
+    d, size = torch.empty_like(l), torch.empty_like(l)
+    for t in range(T):
+        diff = w[t][:, None] - w[t][None, :]
+        own = s[t] * (r[t] * w[t] + (sc[t][None, :] * diff).sum(dim=1))
+        mag = s[t] * (r[t] * w_size[t] + (sc[t][None, :] * diff.abs()).sum(dim=1))
+        rest = -s[t] * (sc[t] * w[t]).sum()
+        d[t] = torch.where(taken[t], own, rest)
+        size[t] = torch.where(taken[t], mag, s[t] * (sc[t] * w_size[t]).sum())
+    slack = s * (w_err + (sc * w_err).sum(dim=1, keepdim=True))
+    return alpha * d, alpha * size, alpha * slack
+
+
+def check_gradient(logits, idx, dw, softmax, norm, alpha=2.5):
+    """Each term is a product of two shares, of rel (far + 32) 2^-24 each with far the distance
+    to the largest logit that enters them, a difference and up to 4 factors (a sigmoid of
+    -l: 6 roundings), in a sum of k + 2; one rounding of the result.  Doubled."""
+    T, E = logits.shape
+    k = idx.shape[1]
+    cfg = nh.gate_config(E, k, 1, 1, norm, alpha, "softmax" if softmax else "sigmoid", "max",
+                         "bf16" if logits.dtype == torch.bfloat16 else "f32")
+    out = torch.full((T + 1, E), 9.0, dtype=logits.dtype, device=DEV)
+    nh.gate_backward(cfg, logits, idx.int(), dw, out[:T])
+    assert (out[T] == 9).all()
+    want, size, slack = gradient_and_size(logits, idx, dw, softmax, norm, alpha)
+    l = ref.clean(logits)
+    over = l if softmax and not norm else l.gather(1, idx)
+    far = (over.amax(dim=1, keepdim=True) - over.amin(dim=1, keepdim=True)).clamp(max=104.0)
+    tol = (size * (2 * (far + 32) + k + 16) * 2.0 ** -23 + 2 * slack +
+           ref.EPS[logits.dtype] * want.abs() + 1e-37)
+    bad = (out[:T].double() - want).abs() > tol
+    assert not bad.any(), (int(bad.sum()), out[:T][bad][:4], want[bad][:4], tol[bad][:4])
+    return out[:T], want
+
+
+@pytest.mark.parametrize("gap", [0.0, 4.0, 8.0, 12.0, 16.0, 30.0])
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_where_one_expert_dominates(gap, softmax, norm, dtype):
+    gen = torch.Generator(device=DEV).manual_seed(int(gap) + 31)
+    for E, k in ((64, 6), (128, 1), (40, 8), (512, 32)):
+        T = 24
+        logits = torch.randn((T, E), generator=gen, device=DEV)
+        if not softmax:
+            logits -= 2.0             # sigmoid shares fall off as exp where logits are low
+        best = torch.randint(0, E, (T, 1), generator=gen, device=DEV)
+        logits = logits.scatter(1, best, logits.amax(dim=1, keepdim=True) + (0.0 if softmax else -gap))
+        logits = (logits - gap).scatter(1, best, logits.gather(1, best)).to(dtype)
+        idx = logits.float().topk(k, dim=1).indices
+        dw = torch.randn((T, k), generator=gen, device=DEV)
+        out, want = check_gradient(logits, idx, dw, softmax, norm)
+        if norm and k == 1:
+            assert (out == 0).all()
+        # the same where the heavy expert was not chosen, and where one is named twice
+        check_gradient(logits, idx.flip(1).roll(1, dims=0), dw, softmax, norm)
+        if k > 1:
+            twice = idx.clone()
+            twice[:, 1] = twice[:, 0]
+            check_gradient(logits, twice, dw, softmax, norm)
+        # against autograd, where that keeps its digits
+        if gap <= 8:
+            g = reference_gradient(logits, idx, dw, softmax, norm, 2.5)
+            assert ((g - want).abs() <= 1e-9 * want.abs().amax(dim=1, keepdim=True) + 1e-12).all()
+
+
+@pytest.mark.parametrize("gap", [8.0, 16.0])
+def test_gradient_rows_of_softmax_sum_to_zero(gap):
+    """sum over experts of dl is 0 for a softmax: what the heavy expert gains the others lose."""
+    gen = torch.Generator(device=DEV).manual_seed(41)
+    T, E, k = 200, 64, 6
+    logits = torch.randn((T, E), generator=gen, device=DEV)
+    logits[:, 5] += gap + 4
+    idx = logits.topk(k, dim=1).indices
+    dw = torch.randn((T, k), generator=gen, device=DEV)
+    for norm in (False, True):
+        out, want = check_gradient(logits, idx, dw, True, norm)
+        total = out.double().sum(dim=1).abs()
+        assert (total <= 2.0 ** -14 * out.double().abs().amax(dim=1)).all()
+
+
 @pytest.mark.parametrize("shape", [(1, 1), (5, 5), (16, 2), (33, 3), (100, 8), (128, 6), (250, 8),
                                    (256, 8), (512, 32)])
 @pytest.mark.parametrize("softmax", [False, True])
