@@ -220,12 +220,13 @@ __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, i
   constexpr bool F32 = OUT == OUT_F32 || OUT == OUT_ADD_F32;
   constexpr int PER = F32 ? 4 : (OUT == OUT_BF16 ? 8 : 16);   // features of a 16-byte word
   constexpr int PASSES = COLS / (8 * PER);
+  const int mine = row0 + min(lane, rows - 1);
   float w = 1.f;          // OUT_RELU2_F8: one over the row's scale
   if constexpr (OUT == OUT_RELU2_F8) {
     const int e = f8::scale_exp(relu_amax(n, acc));
     w = f8::pow2(-e);
     if (lane < rows)
-      g.out_scales[(size_t)(row0 + lane) * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
+      g.out_scales[(size_t)mine * ((g.N + 127) / 128) + f0 / 128] = f8::pow2(e);
   }
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
@@ -254,8 +255,9 @@ __device__ __forceinline__ void finish_rows(const Args& g, int row0, int rows, i
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
       const uint4 word = stage[r * 8 + (j ^ (r & 7))];
+      const int64_t row = row0 + r;
       if (r < rows && c < n) {
-        const size_t at = (size_t)(row0 + r) * g.ldo + f0 + c;
+        const size_t at = (size_t)row * g.ldo + f0 + c;
         if constexpr (OUT == OUT_ADD_F32)
           red_add_f32x4(static_cast<float*>(g.out) + at, __uint_as_float(word.x),
                         __uint_as_float(word.y), __uint_as_float(word.z), __uint_as_float(word.w));
