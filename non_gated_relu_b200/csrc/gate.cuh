@@ -82,7 +82,7 @@ __device__ __forceinline__ void load_row(const float* row, int E, int lane, floa
 #pragma unroll
     for (int i = 0; i + 3 < PER; i += 4) {
       float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (e0 + i < E) v = __ldg(reinterpret_cast<const float4*>(row + e0 + i));
+      if (e0 + i < E) v = *reinterpret_cast<const float4*>(row + e0 + i);
       l[i] = clean(v.x);
       l[i + 1] = clean(v.y);
       l[i + 2] = clean(v.z);
@@ -90,7 +90,7 @@ __device__ __forceinline__ void load_row(const float* row, int E, int lane, floa
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? clean(__ldg(row + e0 + i)) : -INFINITY;
+    for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? clean(row[e0 + i]) : -INFINITY;
   }
 }
 
@@ -102,7 +102,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* row, int E, int la
 #pragma unroll
     for (int i = 0; i + 3 < PER; i += 4) {
       uint2 u = make_uint2(0xff80ff80u, 0xff80ff80u);   // -inf
-      if (e0 + i < E) u = __ldg(reinterpret_cast<const uint2*>(row + e0 + i));
+      if (e0 + i < E) u = *reinterpret_cast<const uint2*>(row + e0 + i);
       l[i] = clean(__uint_as_float(u.x << 16));
       l[i + 1] = clean(__uint_as_float(u.x & 0xffff0000u));
       l[i + 2] = clean(__uint_as_float(u.y << 16));
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER <= 8 ? 5 : 3) gate_forward(con
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (l[i] != -INFINITY) c[i] += __ldg(a.bias + e0 + i);   // past E, too, l is -inf
+        if (l[i] != -INFINITY) c[i] += a.bias[e0 + i];   // past E, too, l is -inf
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] += 0.0f;

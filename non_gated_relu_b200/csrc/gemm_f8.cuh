@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int n = min(COLS, g.N - f0);           // <= 0: no features in this half
       const float* xs = g.xs + (size_t)(ent.y + min(first + lane, ent.z - 1)) * nk;
       const float* ws = g.ws + ((size_t)ent.x * ((g.N + 127) / 128) + (n > 0 ? f0 / 128 : 0)) * nk;
-      float sx = __ldg(xs), sw = __ldg(ws);
+      float sx = *xs, sw = *ws;
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (n > 0) tmem_ld32(from, v0);
         const float s = sx * sw;
         if (kb + 1 < nk) {
-          sx = __ldg(xs + kb + 1);
-          sw = __ldg(ws + kb + 1);
+          sx = xs[kb + 1];
+          sw = ws[kb + 1];
         }
         if (n > 0) {
           tmem_wait();

@@ -287,13 +287,13 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       const int4 ent = entry<NT>(g, t.m);
       const float* ws = g.ws + ((size_t)ent.x * n_blocks + t.nb) * nk;
       const float* xs[CL];
-      float sx[CL], sw = __ldg(ws);
+      float sx[CL], sw = *ws;
 #pragma unroll
       for (int i = 0; i < CL; ++i) {
         // columns past the entry repeat its last row and are not stored
         const int c = half * NC + min(lane + 32 * i, NC - 1);
         xs[i] = g.xs + (size_t)(ent.y + min(c, ent.z - 1)) * nk;
-        sx[i] = __ldg(xs[i]);
+        sx[i] = *xs[i];
       }
       float acc[NC];
 #pragma unroll
@@ -308,9 +308,9 @@ __global__ void __launch_bounds__(THREADS, CTAS)
           if (lane + 32 * i < NC) scales[lane + 32 * i] = sx[i] * sw;
         __syncwarp();
         if (kb + 1 < nk) {
-          sw = __ldg(ws + kb + 1);
+          sw = ws[kb + 1];
 #pragma unroll
-          for (int i = 0; i < CL; ++i) sx[i] = __ldg(xs[i] + kb + 1);
+          for (int i = 0; i < CL; ++i) sx[i] = xs[i][kb + 1];
         }
         ok = __all_sync(0xffffffffu, mbar_wait_spin(tfull_bar(a), (use / NBUF) & 1u, wc, SITE_TC_EPILOGUE));
         if (!ok) break;

@@ -60,7 +60,7 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) f8_gemv(const Args a) {
         wv[u][2 * h] = in ? load_stream(w0 + off) : zero;
         wv[u][2 * h + 1] = in ? load_stream(w1 + off) : zero;
       }
-      sw[u] = b < a.KB ? __ldg(ws + b) : 0.f;
+      sw[u] = b < a.KB ? ws[b] : 0.f;
     }
     if (!waited) wait_previous();
 #pragma unroll

@@ -900,8 +900,7 @@ static nh_status run_gemm(const Plan& p, const GemmCall& c, int dev, cudaStream_
 // ----------------------------------------------------------------------------
 // y = dtype(y_acc): the one rounding of the block output, after the routed
 // experts' weighted combine and the shared expert were added into y_acc
-__global__ void cast_output_bf16x8(const float4* __restrict__ y_acc, uint4* __restrict__ y,
-                                   int64_t n8) {
+__global__ void cast_output_bf16x8(const float4* y_acc, uint4* y, int64_t n8) {
   pdl_wait();
   pdl_trigger();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8;
@@ -913,7 +912,7 @@ __global__ void cast_output_bf16x8(const float4* __restrict__ y_acc, uint4* __re
 }
 
 template <typename Tout>
-__global__ void cast_output(const float* __restrict__ y_acc, Tout* __restrict__ y, int64_t n) {
+__global__ void cast_output(const float* y_acc, Tout* y, int64_t n) {
   pdl_wait();
   pdl_trigger();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;

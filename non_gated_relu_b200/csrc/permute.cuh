@@ -43,10 +43,14 @@ __device__ __forceinline__ int4 expert_tile(int e, int off, int total, int tile_
   return make_int4(e, off + r0, rows, kind);
 }
 
+// Pointers to what the launch before may have written (ids, weights, counts, rows, a
+// latent block's x) are not const __restrict__ in these kernels: that allows loads through the
+// read-only path, which wants memory that nobody writes while the grid lives, and a grid
+// may become resident while the one before it still runs.
+//
 // per-chunk expert histogram: chunk_counts[c][e]
-__global__ void __launch_bounds__(256) permute_hist(const int32_t* __restrict__ idx, int T, int k,
-                                                    int E, int32_t* __restrict__ chunk_counts,
-                                                    int* status) {
+__global__ void __launch_bounds__(256) permute_hist(const int32_t* idx, int T, int k, int E,
+                                                    int32_t* chunk_counts, int* status) {
   extern __shared__ int hist[];
   pdl_wait();
   pdl_trigger();
@@ -147,9 +151,8 @@ __global__ void permute_scan(int32_t* __restrict__ chunk_counts, int n_chunks, i
 constexpr int SCATTER_WARPS = 8;
 
 __global__ void __launch_bounds__(SCATTER_WARPS * 32) permute_scatter(
-    const int32_t* __restrict__ idx, const float* __restrict__ w, int T, int k, int E,
-    const int32_t* __restrict__ chunk_base, int32_t* __restrict__ perm_token,
-    float* __restrict__ perm_w, int32_t* __restrict__ inv_row) {
+    const int32_t* idx, const float* w, int T, int k, int E, const int32_t* chunk_base,
+    int32_t* perm_token, float* perm_w, int32_t* inv_row) {
   extern __shared__ int sm[];
   pdl_wait();
   pdl_trigger();
@@ -243,8 +246,8 @@ constexpr int GATHER_CH = 8;
 
 template <typename Tin>
 __global__ void __launch_bounds__(256) permute_gather(const Tin* __restrict__ x,
-                                                      const int32_t* __restrict__ inv_row, int T,
-                                                      int k, int H, Tin* __restrict__ x_perm) {
+                                                      const int32_t* inv_row, int T, int k, int H,
+                                                      Tin* x_perm) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(256) permute_gather(const Tin* __restrict__ x,
 // memory; warp_sums [33] is shared memory.
 template <typename Tin>
 __device__ __forceinline__ void permute_block(
-    const int32_t* idx, const float* w, const Tin* __restrict__ x, int T, int k, int E, int H,
+    const int32_t* idx, const float* w, const Tin* x, int T, int k, int E, int H,
     int tile_rows, int attach, int max_tiles, int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets,
     int4* __restrict__ tiles, int32_t* __restrict__ num_tiles, int32_t* __restrict__ perm_token,
@@ -384,9 +387,8 @@ struct PermuteOut {
 // Whole permute in one block for T <= PERM_CHUNK tokens (decode).
 // blockDim.x = 512 (>= E).  Dynamic smem: int cnt[E] + int pos[T * k].
 template <typename Tin>
-__global__ void __launch_bounds__(512) permute_small(const int32_t* __restrict__ idx,
-                                                     const float* __restrict__ w,
-                                                     const Tin* __restrict__ x, int T, int k, int E,
+__global__ void __launch_bounds__(512) permute_small(const int32_t* idx, const float* w,
+                                                     const Tin* x, int T, int k, int E,
                                                      int H, PermuteOut o) {
   extern __shared__ int sm[];
   __shared__ int warp_sums[33];

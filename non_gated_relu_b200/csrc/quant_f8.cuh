@@ -140,11 +140,15 @@ __device__ __forceinline__ uint4 encode16(const R& r, float inv) {
 // Rows of activations.  inv_row == null: codes [R, K], scales [R, KB].  With
 // inv_row [R, k]: each row is stored to its k permuted rows instead (ids < 0:
 // no row), so the routed experts read their tokens in expert order.
+//
+// Here and in the kernels that read what this one writes, nothing that a launch
+// before may have written goes through the read-only path (__ldg, or const with
+// __restrict__): that path wants memory which nobody writes while the grid lives, and a
+// grid may become resident while the one before it still runs.
 template <typename Tin>
-__global__ void __launch_bounds__(256) quantize_rows(const Tin* __restrict__ x, uint32_t units,
-                                                     int K, int KB, uint8_t* __restrict__ codes,
-                                                     float* __restrict__ scales,
-                                                     const int32_t* __restrict__ inv_row, int k) {
+__global__ void __launch_bounds__(256) quantize_rows(const Tin* x, uint32_t units, int K, int KB,
+                                                     uint8_t* codes, float* scales,
+                                                     const int32_t* inv_row, int k) {
   pdl_wait();
   pdl_trigger();
   const int sub = threadIdx.x & 7;
@@ -164,11 +168,16 @@ __global__ void __launch_bounds__(256) quantize_rows(const Tin* __restrict__ x, 
       if (col < K) *reinterpret_cast<uint4*>(codes + (size_t)row * K + col) = q;
       if (sub == 0) scales[u] = pow2(e);
     } else {
-      for (int j = 0; j < k; ++j) {
-        const int p = __ldg(inv_row + (size_t)row * k + j);
-        if (p < 0) continue;
-        if (col < K) *reinterpret_cast<uint4*>(codes + (size_t)p * K + col) = q;
-        if (sub == 0) scales[(size_t)p * KB + b] = pow2(e);
+      for (int j0 = 0; j0 < k; j0 += 8) {
+        int to[8];           // asked for together, ahead of the stores
+#pragma unroll
+        for (int j = 0; j < 8; ++j) to[j] = j0 + j < k ? inv_row[(size_t)row * k + j0 + j] : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (to[j] < 0) continue;
+          if (col < K) *reinterpret_cast<uint4*>(codes + (size_t)to[j] * K + col) = q;
+          if (sub == 0) scales[(size_t)to[j] * KB + b] = pow2(e);
+        }
       }
     }
   }
@@ -176,10 +185,8 @@ __global__ void __launch_bounds__(256) quantize_rows(const Tin* __restrict__ x, 
 
 // One 128 x 128 block of a weight per CTA: thread = half a row (64 values).
 template <typename Tin>
-__global__ void __launch_bounds__(256) quantize_blocks(const Tin* __restrict__ w, int rows,
-                                                       int cols, int RB, int CB,
-                                                       uint8_t* __restrict__ codes,
-                                                       float* __restrict__ scales) {
+__global__ void __launch_bounds__(256) quantize_blocks(const Tin* w, int rows, int cols, int RB,
+                                                       int CB, uint8_t* codes, float* scales) {
   __shared__ uint32_t part[8];
   pdl_wait();
   pdl_trigger();
