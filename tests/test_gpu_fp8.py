@@ -810,3 +810,122 @@ def test_experts_add_to_what_is_there():
         nh.permute(c, x, idx, w, ws)
         nh.forward_fp8(c, x, nh.fp8_weight(*up), nh.fp8_weight(*down), ws, y)
         assert torch.equal(y, start + alone)      # one float32 add
+
+
+# -- launches that follow one another closely ----------------------------------------------
+@pytest.mark.parametrize("T", [9, 16, 32, 33, 64, 700, 2000])
+def test_linear_right_after_the_weights_are_made_any_kernel(T):
+    """No weight or scale is read ahead of the kernel that makes it: the GEMV behind the
+    quantization, small tiles and pairs."""
+    gen = generator(T + 50)
+    N, K = 512, 1024
+    x = torch.randn((T, K), generator=gen, device=DEV).to(B16)
+    sets = [torch.randn((1, N, K), generator=gen, device=DEV).to(B16) * 2.0 ** i for i in range(4)]
+    codes = torch.empty((1, N, K), dtype=torch.float8_e4m3fn, device=DEV)
+    scales = torch.empty((1, N // 128, K // 128), device=DEV)
+    w = nh.fp8_weight(codes, scales)
+    ws = torch.zeros(nh.fp8_linear_workspace_size(T, N, K), dtype=torch.uint8, device=DEV)
+    want = []
+    for v in sets:
+        nh.fp8_quantize_weight(v, codes, scales)
+        torch.cuda.synchronize()
+        y = torch.empty((T, N), device=DEV)
+        nh.fp8_linear(x, w, y, ws)
+        torch.cuda.synchronize()
+        want.append(y)
+    got = [torch.empty((T, N), device=DEV) for _ in range(24)]
+    for i, y in enumerate(got):
+        nh.fp8_quantize_weight(sets[i % 4], codes, scales)
+        nh.fp8_linear(x, w, y, ws)
+    torch.cuda.synchronize()
+    assert nh.check_device(ws) == 0
+    assert all(torch.equal(y, want[i % 4]) for i, y in enumerate(got))
+
+
+@pytest.mark.parametrize("T", [1, 8, 32, 33, 200, 1500])
+@pytest.mark.parametrize("split", [False, True])
+def test_experts_right_after_weights_and_routing_change(T, split):
+    """Weights rewritten and the permute made anew directly before each call, on one
+    workspace: neither the weights nor the tile table nor the scales of the call before
+    are seen."""
+    gen = generator(T + 60)
+    cfg = config(T)
+    c = nh.config_from(cfg)
+    E, H, I = cfg.E, cfg.H, cfg.I
+    r = lambda *s: torch.randn(s, generator=gen, device=DEV).to(B16)  # noqa: E731
+    sets = []
+    for i in range(3):
+        idx, w = routing(T, E, cfg.k, gen, skew=2.0)
+        sets.append((r(E, I, H) * 2.0 ** -i, r(E, H, I) * 2.0 ** i, r(T, H), idx, w))
+    up = (torch.empty((E, I, H), dtype=torch.uint8, device=DEV),
+          torch.empty((E, -(-I // 128), -(-H // 128)), device=DEV))
+    down = (torch.empty((E, H, I), dtype=torch.uint8, device=DEV),
+            torch.empty((E, -(-H // 128), -(-I // 128)), device=DEV))
+    fu, fd = nh.fp8_weight(*up), nh.fp8_weight(*down)
+    ws = torch.zeros(nh.workspace_size(c, T), dtype=torch.uint8, device=DEV)
+
+    def go(s, y, apart):
+        pause = torch.cuda.synchronize if apart else (lambda: None)
+        uv, dv, x, idx, w = s
+        nh.zero_acc(c, T, y)
+        nh.permute(c, x, idx, w, ws)
+        pause()
+        if split:
+            nh.fp8_quantize_weight(uv, *up)
+            pause()
+            nh.experts_up_fp8(c, x, fu, ws)
+            pause()
+            nh.fp8_quantize_weight(dv, *down)
+            pause()
+            nh.experts_down_fp8(c, T, fd, ws, y)
+        else:
+            nh.fp8_quantize_weight(uv, *up)
+            nh.fp8_quantize_weight(dv, *down)
+            pause()
+            nh.forward_fp8(c, x, fu, fd, ws, y)
+        pause()
+
+    want = [torch.empty((T, H), device=DEV) for _ in sets]
+    for s, y in zip(sets, want):
+        go(s, y, True)
+    got = [torch.empty((T, H), device=DEV) for _ in range(18)]
+    for i, y in enumerate(got):
+        go(sets[i % 3], y, False)
+    torch.cuda.synchronize()
+    assert nh.check_device(ws) == 0
+    assert all(torch.equal(y, want[i % 3]) for i, y in enumerate(got))
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 32, 33, 300])
+def test_shared_right_after_the_weights_are_made(T):
+    gen = generator(T + 70)
+    cfg = config(T)
+    c = nh.config_from(cfg)
+    H, S = cfg.H, cfg.S
+    r = lambda *s: torch.randn(s, generator=gen, device=DEV).to(B16)  # noqa: E731
+    sets = [(r(1, S, H) * 2.0 ** -i, r(1, H, S) * 2.0 ** i, r(T, H)) for i in range(3)]
+    su = (torch.empty((1, S, H), dtype=torch.uint8, device=DEV),
+          torch.empty((1, -(-S // 128), -(-H // 128)), device=DEV))
+    sd = (torch.empty((1, H, S), dtype=torch.uint8, device=DEV),
+          torch.empty((1, -(-H // 128), -(-S // 128)), device=DEV))
+    fu, fd = nh.fp8_weight(*su), nh.fp8_weight(*sd)
+    ws = torch.zeros(nh.shared_workspace_size(c, T), dtype=torch.uint8, device=DEV)
+
+    def go(s, y, apart):
+        nh.fp8_quantize_weight(s[0], *su)
+        nh.fp8_quantize_weight(s[1], *sd)
+        if apart:
+            torch.cuda.synchronize()
+        nh.shared_store_fp8(c, s[2], fu, fd, y, ws)
+        if apart:
+            torch.cuda.synchronize()
+
+    want = [torch.empty((T, H), device=DEV) for _ in sets]
+    for s, y in zip(sets, want):
+        go(s, y, True)
+    got = [torch.empty((T, H), device=DEV) for _ in range(18)]
+    for i, y in enumerate(got):
+        go(sets[i % 3], y, False)
+    torch.cuda.synchronize()
+    assert nh.check_device(ws) == 0
+    assert all(torch.equal(y, want[i % 3]) for i, y in enumerate(got))
