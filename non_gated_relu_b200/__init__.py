@@ -100,17 +100,21 @@ class Layout(ctypes.Structure):
 
 def config_from(c, group_score: int = 0) -> Config:
     """Build the C struct from any object with the config.json attribute names
-    (and ``dtype`` in {"bf16", "f32"})."""
+    (and ``dtype`` in {"bf16", "f32"}; ``weight_format`` "native" (also None or without the
+    field), "nvfp4" or "fp8")."""
     if isinstance(c, Config):
         return c
     dt = getattr(c, "dtype", "bf16")
+    fmt = getattr(c, "weight_format", None)
+    if fmt is not None and fmt not in _WEIGHT_FORMATS:
+        raise ValueError(f"unknown weight_format {fmt!r}")
     return Config(int(c.hidden_size), int(c.n_routed_experts), int(c.n_group), int(c.topk_group),
                   int(c.num_experts_per_tok), int(c.moe_intermediate_size),
                   int(c.moe_shared_expert_intermediate_size), int(c.n_shared_experts),
                   int(bool(c.norm_topk_prob)), float(c.routed_scaling_factor),
                   NH_BF16 if dt in ("bf16", NH_BF16) else NH_F32,
                   int(getattr(c, "group_score", group_score)),
-                  _WEIGHT_FORMATS.get(getattr(c, "weight_format", "native"), NH_WEIGHTS_NATIVE),
+                  NH_WEIGHTS_NATIVE if fmt is None else _WEIGHT_FORMATS[fmt],
                   int(getattr(c, "latent_size", 0) or 0))
 
 
@@ -251,8 +255,18 @@ def shared_workspace_size(cfg, T: int) -> int:
     return n.value
 
 
+def _sigmoid_config(cfg) -> Config:
+    """config_from for the routers whose scores are sigmoids: another ``scoring_func`` in
+    the config is refused."""
+    score = getattr(cfg, "scoring_func", None)
+    if score is not None and _SCORE_FUNCS.get(score) != NH_SCORE_SIGMOID:
+        raise ValueError(f"scoring_func {score!r}: this router's scores are sigmoids, "
+                         "use route_scored")
+    return config_from(cfg)
+
+
 def route(cfg, x, w_router, bias, topk_idx, topk_w, ws, stream=None):
-    c = config_from(cfg)
+    c = _sigmoid_config(cfg)
     _check(load().nh_moe_route(ctypes.byref(c), x.shape[0], _p(x), _p(w_router), _p(bias),
                                _p(topk_idx), _p(topk_w), _p(ws), _nbytes(ws), _stream(stream)))
 
@@ -260,14 +274,14 @@ def route(cfg, x, w_router, bias, topk_idx, topk_w, ws, stream=None):
 def route_noalloc(cfg, x, w_router, bias, topk_idx, topk_w, stream=None):
     """Router of decode-sized batches (T <= 32) without a workspace argument: its
     scratch is a fixed array inside the library (see nh_moe_route_noalloc)."""
-    c = config_from(cfg)
+    c = _sigmoid_config(cfg)
     _check(load().nh_moe_route_noalloc(ctypes.byref(c), x.shape[0], _p(x), _p(w_router),
                                        _p(bias), _p(topk_idx), _p(topk_w), _stream(stream)))
 
 
 def route_permute(cfg, x, w_router, bias, topk_idx, topk_w, ws, stream=None):
     """route + permute in one call (one kernel for T <= 32)."""
-    c = config_from(cfg)
+    c = _sigmoid_config(cfg)
     _check(load().nh_moe_route_permute(ctypes.byref(c), x.shape[0], _p(x), _p(w_router), _p(bias),
                                        _p(topk_idx), _p(topk_w), _p(ws), _nbytes(ws),
                                        _stream(stream)))

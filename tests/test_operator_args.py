@@ -268,3 +268,26 @@ def test_weights_of_another_device_are_refused(monkeypatch):
     monkeypatch.setattr(nh._types(), "current_device", lambda: 0)
     with pytest.raises(ValueError, match="cuda:1"):
         nh._fp8("w", w, (1, 64, 128))
+
+
+def test_unknown_weight_formats_are_refused():
+    base = synth.CONFIGS["tiny_f32_t64"].replace(dtype="bf16", hidden_size=64)
+    for fmt in ("FP8", "fp8_e4m3", "bf16", 3):
+        with pytest.raises(ValueError, match="weight_format"):
+            nh.config_from(base.replace(weight_format=fmt))
+    for fmt, value in (("native", 0), ("nvfp4", 1), ("fp8", 2), (2, 2), (None, 0)):
+        assert nh.config_from(base.replace(weight_format=fmt)).weight_format == value
+
+
+def test_sigmoid_routers_refuse_other_scores():
+    """The routers whose scores are sigmoids do not answer a config that asks for others."""
+    torch = pytest.importorskip("torch")
+    cfg = synth.CONFIGS["tiny_f32_t64"].replace(T=2, scoring_func="softmax")
+    x = torch.zeros((2, cfg.hidden_size))
+    for call in (lambda c: nh.route(c, x, x, None, x, x, x),
+                 lambda c: nh.route_permute(c, x, x, None, x, x, x),
+                 lambda c: nh.route_noalloc(c, x, x, None, x, x)):
+        with pytest.raises(ValueError, match="route_scored"):
+            call(cfg)
+        with pytest.raises(ValueError, match="scoring_func"):
+            call(cfg.replace(scoring_func="sqrtsoftplus"))
