@@ -74,7 +74,7 @@ nh_status nh_fp8_linear(int64_t T, int64_t N, int64_t K, const void* x, int32_t 
   NH_TRY(check_f8(w, "w"));
   NH_TRY(check_ptr(y, "y"));
   int dev;
-  NH_TRY(device_setup(&dev));
+  NH_TRY(f8_device_setup(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* xq = at<uint8_t>(ws, ALIGN);
   float* xs = at<float>(ws, ALIGN + f8_scales_at(T, K));
@@ -163,7 +163,7 @@ static nh_status f8_experts(const nh_moe_config* cfg, int64_t T, const void* x,
   if (up) NH_TRY(check_ptr(x, "x"));
   if (down) NH_TRY(check_ptr(y_acc, "y_acc"));
   int dev;
-  NH_TRY(device_setup(&dev));
+  NH_TRY(f8_device_setup(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (up) NH_TRY(f8_experts_up(p, T, x, w_up, ws, dev, st));
   if (down) NH_TRY(f8_experts_down(p, T, w_down, ws, y_acc, up, dev, st));
@@ -207,7 +207,7 @@ static nh_status f8_shared(const nh_moe_config* cfg, int64_t T, const void* x,
   NH_TRY(check_ptr(x, "x"));
   NH_TRY(check_ptr(y_acc, "y_acc"));
   int dev;
-  NH_TRY(device_setup(&dev));
+  NH_TRY(f8_device_setup(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int* status = static_cast<int*>(ws);
   NH_CUDA(cudaMemsetAsync(status, 0, STATUS_BYTES, st));

@@ -324,8 +324,10 @@ constexpr int MAX_DEVICES = 64;
 static std::once_flag g_attr_once[MAX_DEVICES];
 static int g_sm_count[MAX_DEVICES];
 static int g_pair_clusters[MAX_DEVICES];  // co-resident 2-CTA clusters of tc2_grouped_gemm
-static int g_f8_clusters[MAX_DEVICES];    // and of f8_pair_gemm
 static nh_status g_attr_status[MAX_DEVICES];
+static std::once_flag g_f8_once[MAX_DEVICES];
+static int g_f8_clusters[MAX_DEVICES];    // co-resident 2-CTA clusters of f8_pair_gemm
+static nh_status g_f8_status[MAX_DEVICES];
 
 using TcPrefill = tc::Shape<false, 256, 4>;
 using TcPrefill128 = tc::Shape<false, 128, 6>;
@@ -361,6 +363,27 @@ static nh_status f8_swap_attrs() {
   return NH_OK;
 }
 
+// CTA pairs of a kernel that fit on the device at once
+template <typename Kern>
+static nh_status pair_clusters(Kern kernel, int threads, int smem, const char* what, int dev,
+                               int* clusters) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(2 * (g_sm_count[dev] / 2), 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  NH_CUDA(cudaOccupancyMaxActiveClusters(clusters, kernel, &lc));
+  if (*clusters < 1)
+    return fail(NH_ERR_UNSUPPORTED, "no 2-CTA cluster of the %s GEMM fits on device %d", what, dev);
+  return NH_OK;
+}
+
 static nh_status set_attrs(int dev) {
   cudaDeviceProp prop;
   NH_CUDA(cudaGetDeviceProperties(&prop, dev));
@@ -390,6 +413,11 @@ static nh_status set_attrs(int dev) {
                                cudaFuncAttributeMaxDynamicSharedMemorySize, ROUTE_PERMUTE_SMEM_MAX));
   NH_CUDA(cudaFuncSetAttribute(route_permute_small<float>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, ROUTE_PERMUTE_SMEM_MAX));
+  return pair_clusters(tc2::tc2_grouped_gemm, tc2::THREADS, tc2::SMEM, "pair", dev,
+                       &g_pair_clusters[dev]);
+}
+
+static nh_status set_f8_attrs(int dev) {
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_BF16>));
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_F32>));
   NH_TRY(f8_pair_attrs(f8g::f8_pair_gemm<f8g::OUT_RELU2_F8>));
@@ -397,29 +425,8 @@ static nh_status set_attrs(int dev) {
   NH_TRY((f8_swap_attrs<16, 5, 2>()));
   NH_TRY((f8_swap_attrs<32, 5, 2>()));
   NH_TRY((f8_swap_attrs<64, 4, 2>()));
-  {
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(2 * (prop.multiProcessorCount / 2), 1, 1);
-    lc.blockDim = dim3(tc2::THREADS, 1, 1);
-    lc.dynamicSmemBytes = tc2::SMEM;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    int n = 0;
-    NH_CUDA(cudaOccupancyMaxActiveClusters(&n, tc2::tc2_grouped_gemm, &lc));
-    if (n < 1) return fail(NH_ERR_UNSUPPORTED, "no 2-CTA cluster of the pair GEMM fits on device %d", dev);
-    g_pair_clusters[dev] = n;
-    lc.blockDim = dim3(f8g::THREADS, 1, 1);
-    lc.dynamicSmemBytes = f8g::SMEM;
-    NH_CUDA(cudaOccupancyMaxActiveClusters(&n, f8g::f8_pair_gemm<f8g::OUT_F32>, &lc));
-    if (n < 1) return fail(NH_ERR_UNSUPPORTED, "no 2-CTA cluster of the FP8 GEMM fits on device %d", dev);
-    g_f8_clusters[dev] = n;
-  }
-  return NH_OK;
+  return pair_clusters(f8g::f8_pair_gemm<f8g::OUT_F32>, f8g::THREADS, f8g::SMEM, "FP8 pair", dev,
+                       &g_f8_clusters[dev]);
 }
 
 static nh_status device_setup(int* dev_out) {
@@ -430,6 +437,17 @@ static nh_status device_setup(int* dev_out) {
   if (g_attr_status[dev] != NH_OK)
     return fail(g_attr_status[dev], "device %d setup failed (unsupported or CUDA error)", dev);
   *dev_out = dev;
+  return NH_OK;
+}
+
+// For the FP8 products: a build or a device that their kernels do not fit refuses
+// them, not the calls that need none of them.
+static nh_status f8_device_setup(int* dev_out) {
+  NH_TRY(device_setup(dev_out));
+  const int dev = *dev_out;
+  std::call_once(g_f8_once[dev], [dev] { g_f8_status[dev] = set_f8_attrs(dev); });
+  if (g_f8_status[dev] != NH_OK)
+    return fail(g_f8_status[dev], "device %d: FP8 setup failed (unsupported or CUDA error)", dev);
   return NH_OK;
 }
 

@@ -31,3 +31,19 @@ def test_no_read_only_loads_of_what_a_launch_before_may_write():
             assert "permute_gather" in k and arg == "x", (arg, k)
     cast = re.findall(r"__global__ void cast_output\w*\((.*?)\)", code("nh_moe.cu"), flags=re.S)
     assert len(cast) == 2 and not any("__restrict__" in c for c in cast)
+
+
+def test_only_fp8_products_need_the_fp8_kernels():
+    """A build or device that the FP8 products do not fit refuses those calls alone: the
+    setup that every other call waits for does not look at their kernels."""
+    text = code("nh_moe.cu")
+    body = text[text.index("static nh_status set_attrs("):text.index("static nh_status set_f8_attrs(")]
+    assert "f8" not in body.lower()
+    assert len(re.findall(r"\bf8_device_setup\(&dev\)", text)) == 0
+    api = code("api_f8.cuh")
+    entry = {m.group(1): m.group(0) for m in re.finditer(
+        r"^(?:static )?nh_status (\w+)\([^{]*\{.*?^\}", api, flags=re.S | re.M)}
+    for name in ("nh_fp8_linear", "f8_experts", "f8_shared"):
+        assert "f8_device_setup(&dev)" in entry[name], name
+    for name in ("nh_fp8_quantize", "nh_fp8_quantize_weight"):
+        assert "f8_device_setup" not in entry[name], name
