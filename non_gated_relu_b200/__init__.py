@@ -553,21 +553,36 @@ def fp8_quantize(x, codes, scales, stream=None):
     _check((_lib or load()).nh_fp8_quantize(T, K, px, _dt(x), pc, ps, _stream(stream)))
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that a launch on `stream` writes.  torch hands memory out in the order of
+    one stream's work: what the current stream still does to its last owner is not done
+    when another stream's kernel starts."""
+    torch = _types().torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def fp8_quantize_weight(w, codes=None, scales=None, stream=None):
     """w [n, rows, cols] (bfloat16 or float32) as FP8: returns (codes, scales), which
-    are allocated where they are not given."""
-    import torch
+    are allocated where they are not given (on `stream`, for use on the current one, too)."""
     ty = _types()
     if w.dim() != 3:
         raise ValueError(f"w: expected [n, rows, cols], got {tuple(w.shape)}")
     n, rows, cols = w.shape
     blocks = (n, -(-rows // 128), -(-cols // 128))
+    wspec = ("w", w, ty.act, (n, rows, cols))
+    _args(wspec)
     if codes is None:
-        codes = torch.empty((n, rows, cols), dtype=torch.float8_e4m3fn, device=w.device)
+        codes = _empty((n, rows, cols), ty.torch.float8_e4m3fn, w.device, stream)
     if scales is None:
-        scales = torch.empty(blocks, dtype=torch.float32, device=w.device)
-    pw, pc, ps = _args(("w", w, ty.act, (n, rows, cols)), ("codes", codes, ty.f8, (n, rows, cols)),
-                       ("scales", scales, ty.f32, blocks))
+        scales = _empty(blocks, ty.torch.float32, w.device, stream)
+    pw, pc, ps = _args(wspec, ("codes", codes, ty.f8, (n, rows, cols)), ("scales", scales, ty.f32, blocks))
     _check((_lib or load()).nh_fp8_quantize_weight(n, rows, cols, pw, _dt(w), pc, ps, _stream(stream)))
     return codes, scales
 

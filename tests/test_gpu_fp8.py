@@ -929,3 +929,24 @@ def test_shared_right_after_the_weights_are_made(T):
     torch.cuda.synchronize()
     assert nh.check_device(ws) == 0
     assert all(torch.equal(y, want[i % 3]) for i, y in enumerate(got))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_weights_allocated_for_another_stream(handle):
+    """Codes and scales that the call allocates may lie where the current stream still works
+    for a tensor that is gone: its last write must not reach them."""
+    gen = generator(83)
+    w = torch.randn((1, 2048, 4096), generator=gen, device=DEV)
+    want = nh.fp8_quantize_weight(w)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    old = [torch.empty(t.numel() * t.element_size(), dtype=torch.uint8, device=DEV) for t in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)            # some 20 ms of the current stream
+    for t in old:
+        t.fill_(0x55)
+    del t, old
+    got = nh.fp8_quantize_weight(w, stream=side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
