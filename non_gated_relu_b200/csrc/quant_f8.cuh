@@ -220,32 +220,38 @@ __global__ void __launch_bounds__(256) quantize_blocks(const Tin* w, int rows, i
 // leaves a token's k rows apart and they meet here, so a result does not depend on
 // the order in which tiles end.  Adding tiles to y_acc as they end does, and saves a
 // launch and the rows' way to memory and back: 128 experts of 2688 x 1856, 6 taken, in
-// a graph with this kernel and without: 8 tokens 76 and 72 us, 301 tokens 241 and 235,
+// a graph with this kernel and without: 8 tokens 75 and 72 us, 301 tokens 241 and 235,
 // 16384 tokens 1.95 and 1.79 ms.  One add to an element of y_acc, atomic, since the
 // shared expert may add to it at the same time.  `parts` blocks share a token, a thread
 // holds four features; rows of eight slots are asked for at once.
 __global__ void __launch_bounds__(256) combine_rows(const float* rows, const int32_t* inv_row,
                                                     const float* perm_w, int parts, int k,
                                                     int quads, float* y_acc) {
-  pdl_wait();
-  pdl_trigger();
   const int t = blockIdx.x / parts;
   const int q = (blockIdx.x - t * parts) * blockDim.x + threadIdx.x;
+  int row[8];
+  float w[8];
+  auto slots = [&](int j0) {       // rows and weights of slots j0 ..; no row: id out of range
+#pragma unroll
+    for (int j = 0; j < 8; ++j) row[j] = j0 + j < k ? inv_row[(size_t)t * k + j0 + j] : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = row[j] >= 0 ? perm_w[row[j]] : 0.f;
+  };
+  // The permute was complete before the down projection, the launch before, began: the
+  // first slots are asked for ahead of the wait for its rows.
+  slots(0);
+  pdl_wait();
+  pdl_trigger();
   if (q >= quads) return;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j0 = 0; j0 < k; j0 += 8) {
-    float w[8];
+    if (j0) slots(j0);
     float4 v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = j0 + j < k ? inv_row[(size_t)t * k + j0 + j] : -1;
-      w[j] = 0.f;
-      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r >= 0) {          // an id out of range has no row
-        w[j] = perm_w[r];
-        v[j] = __ldcs(reinterpret_cast<const float4*>(rows) + (size_t)r * quads + q);
-      }
-    }
+    for (int j = 0; j < 8; ++j)
+      v[j] = row[j] >= 0
+                 ? __ldcs(reinterpret_cast<const float4*>(rows) + (size_t)row[j] * quads + q)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       sum.x = fmaf(w[j], v[j].x, sum.x);
