@@ -497,7 +497,7 @@ nh_status nh_fp8_quantize_weight(int64_t n_mat, int64_t rows, int64_t cols, cons
  * y = x W^T with E4M3 operands: x is quantized as by nh_fp8_quantize, and
  *   y[t, n] = sum over blocks b of 128 features of
  *             s_x[t, b] s_w[n / 128, b] (codes of x[t] . codes of W[n] in block b)
- * with float32 products and sums, rounded once to y's dtype.
+ * with float32 products and sums (s_x s_w is taken first), rounded once to y's dtype.
  *   x [T, K] x_dtype; w: nh_fp8_weight [1][N][K]; y [T, N] y_dtype (out);
  *   N and K multiples of 16; ws: nh_fp8_linear_workspace_size bytes, 256-byte
  *   aligned, holding a status word (cleared by the caller, once:

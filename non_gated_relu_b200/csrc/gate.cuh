@@ -13,8 +13,9 @@
 // two experts the logits order the experts as their scores do, so the float32
 // logits are compared themselves.  Otherwise c is computed in float32 first;
 // a token in which two neighbours that the choice or its order depends on are
-// closer than the float32 error of c (and are not the same logit and bias) is
-// chosen again from scores in 64 bits, by the same warp.
+// closer than the float32 error of c (and are not the same logit and bias), or a
+// kept and a dropped group closer than theirs, is chosen again from scores in 64
+// bits, by the same warp.
 //
 // Weights are computed from the chosen logits alone where norm is set, scaled
 // by the largest of them (softmax) or by min(0, largest) (sigmoid), so that
@@ -25,8 +26,9 @@
 // integer max over the warp (redux) on order-preserving keys.  Bound by
 // instruction issue (about 1200 a token with groups, bias and 256 experts, the
 // compare and integer pipe first): 16384 tokens, 256 experts, sigmoid, bias, 4 of 8
-// groups by their two best: 25 us; 128 experts, softmax, one of 8 groups: 16 us;
-// the gradient 8 us, where its bytes would take 2.8.
+// groups by their two best: 26 to 31 us a call (bf16 logits without a bias, whose
+// exact ties at the k-th place go to 64 bits: 34); the gradient 9.4 us, where its
+// bytes would take 2.8.
 #pragma once
 
 #include "common.cuh"

@@ -15,9 +15,11 @@
 // takes its 128 columns in four loads, each in flight while the one before is
 // added, and hands the accumulator back before it adds the last.  They wait without
 // the sleep hint (a K block of a lone pair 461 -> 449 ns).  Measured: a K
-// block every 700 to 850 cycles and 2000 to 3500 for the end of a tile; 16384 x
-// 3712 x 2688 in 163 us (2.0 PFLOP/s, at the power limit), the experts' two
-// products of 16384 tokens (128 experts of 2688 x 1856, 6 taken) in 663 and 785.
+// block every 700 to 850 cycles and 2000 to 3500 for the end of a tile.  One launch at
+// a time, under the profiler: 16384 x 3712 x 2688 in 160 us (2.0 PFLOP/s), the experts'
+// two products of 16384 tokens (128 experts of 2688 x 1856, 6 taken) in 652 and 722.
+// Calls one after the other run at the power limit: the linear call takes 207 us, 22 of
+// them the quantization, the experts' 1.95 ms.
 // A thread owns one row and 128 features, which makes the
 // scale one number per thread and block, and leaves the maximum of a (row, 128
 // features) block of the output inside one thread, where the next projection's

@@ -11,9 +11,9 @@
 // NT, four of K = 32 from zero) take a fraction of the time the weights take to
 // arrive, and the rate is that of memory as long as enough bytes are under way:
 // two CTAs per SM, each with about 100 KB of stages (one CTA of 192 KB, as 128
-// rows a tile would need, drew 3.7 TB/s where two draw 6).  Measured: 64 tokens,
-// 6 of 128 experts of 2688 x 1856 each, 116 experts hit: 92 us for each of the two
-// projections, 6.3 TB/s; 8 tokens (37 hit): 33 and 32 us, 5.6 TB/s.  As in
+// rows a tile would need, drew 3.7 TB/s where two draw 6).  Measured, one launch at
+// a time under the profiler, 6 of 128 experts of 2688 x 1856 taken: 301 tokens (all
+// hit): 106 and 107 us for the two projections, 6.0 TB/s; 8 tokens: 35 and 35.  As in
 // the pair kernel each K block is its own accumulator, four in turn, drained
 // into registers times its scales by eight warps (warp w: weight rows of quarter
 // w mod 4, half of the columns); the weight scale is one number per block and the

@@ -169,9 +169,10 @@ static void tile_plan(const nh_moe_config* c, int64_t T, int* tile_rows, int* sw
     *swap = 1;
   } else if (c->weight_format == NH_WEIGHTS_FP8) {
     // Weights on the MMA M side while an expert has few rows (the mean of T k / E).
-    // Measured on 128 experts of 2688 x 1856, us at 16 / 32 / 64 / 256 rows a tile:
-    // mean 0.4: 68 / 70 / 83 / 127; mean 24: - / 246 / 253 / 423; mean 48: - / 297 /
-    // 282 / 435; mean 96: - / 463 / 391 / 477; mean 192: - / 814 / 652 / 588.
+    // Measured on 128 experts of 2688 x 1856, the whole call in a graph, us at 16 / 32 /
+    // 64 / 256 rows a tile: mean 0.4: 74 / 75 / 89 / 132; mean 3: 188 / 192 / 210 / 371;
+    // mean 24: 290 / 261 / 269 / 472; mean 48: 443 / 339 / 329 / 491; mean 96: 749 / 542 /
+    // 478 / 535; mean 192: 1373 / 938 / 803 / 699.
     const int64_t mean = T * c->num_experts_per_tok / c->n_routed_experts;
     *tile_rows = mean <= 3 ? 16 : (mean <= 32 ? 32 : (mean <= 128 ? 64 : f8g::MP));
     *swap = *tile_rows < f8g::MP ? 1 : 0;
