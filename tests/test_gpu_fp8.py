@@ -950,3 +950,29 @@ def test_weights_allocated_for_another_stream(handle):
     got = nh.fp8_quantize_weight(w, stream=side.cuda_stream if handle else side)
     torch.cuda.synchronize()
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+
+
+def test_experts_with_rows_past_32_bits():
+    """Codes, down-projection rows and their offsets past 2^32: a batch that repeats one of
+    1000 tokens gives the small batch's result in every repetition, bit for bit (both run
+    on tiles of the same height, and a row's sums do not depend on its place)."""
+    P, R = 1000, 270
+    cfg = config(P, hidden_size=1024, moe_intermediate_size=64, n_routed_experts=16, n_group=1,
+                 topk_group=1, num_experts_per_tok=16)
+    assert R * P * cfg.k * cfg.H > 2 ** 32
+    if torch.cuda.mem_get_info()[0] < 60 * 2 ** 30:
+        pytest.skip("needs 60 GB")
+    c, gen = nh.config_from(cfg), generator(91)
+    assert nh.workspace_layout(c, P).tile_rows == nh.workspace_layout(c, P * R).tile_rows
+    up, down = experts_case(cfg, gen)
+    idx, w = routing(P, cfg.E, cfg.k, gen)
+    x = torch.randn((P, cfg.H), generator=gen, device=DEV).to(B16)
+    want, *_ = run_experts(cfg, x, idx, w, up, down)
+    T = P * R
+    ws = torch.zeros(nh.workspace_size(c, T), dtype=torch.uint8, device=DEV)
+    y = torch.zeros((T, cfg.H), device=DEV)
+    xs, idxs, wts = x.repeat(R, 1), idx.repeat(R, 1), w.repeat(R, 1)
+    nh.permute(c, xs, idxs, wts, ws)
+    nh.forward_fp8(c, xs, nh.fp8_weight(*up), nh.fp8_weight(*down), ws, y)
+    assert nh.check_device(ws) == 0
+    assert (y.view(R, P, cfg.H) == want).all()
